@@ -4,8 +4,10 @@
  * pkm_gather; pkm_forward_host / pkm_forward_host_async with host buffers;
  * the allocation-free pkm_lookup_static), its backward pass for the selection
  * it made (pkm_backward, pkm_backward_sparse and their two parts), the query
- * network ahead of it (pkm_bn_fold, pkm_query_net) and the fp8 value-table
- * quantiser (pkm_quantize_values_fp8).
+ * network ahead of it (pkm_bn_fold, pkm_query_net), the fp8 value-table
+ * quantiser (pkm_quantize_values_fp8), and two operators of the model around
+ * it with their gradients: the gated feed-forward block (pkm_gated_ffn) and
+ * distillation from a teacher's top logits (pkm_distill).
  *
  * The operation (Product-Key Memory, "Factorising the key space", and the
  * forward method of the page's code listing; Memory Retrieval Mechanisms,
@@ -438,6 +440,106 @@ size_t pkm_query_net_batch_workspace_bytes(int B, int F);
 int pkm_query_net_batch(const void *x, const void *weight, int B, int dim, int F,
                         const float *gamma, const float *beta, float eps, void *workspace, void *q,
                         float *batch_mean, float *batch_var, int *status, void *stream);
+
+/*
+ * The gated feed-forward block: the dense block of a transformer that a
+ * product-key memory layer stands beside or in place of ("You could have
+ * invented transformers from memory", MLP as a nonlinear memory store).
+ *
+ *   g = x Wg^T,  u = x Wu^T,  h = act(g) * u,  y = h Wd^T
+ *
+ * x [B, dim], Wg (w_gate) and Wu (w_up) [F, dim], Wd (w_down) [dim, F], y
+ * [B, dim], all bf16, row-major and contiguous (nn.Linear's weight layout);
+ * dim and F multiples of 8; tensor cores, fp32 accumulation.  h is rounded
+ * to bf16 once, between the two products.
+ *
+ * pkm_gated_ffn: y, and, when gate and up are not NULL (both or neither), g
+ * and u [B, F] in bf16, which the backward pass reads.  workspace: device
+ * scratch of pkm_gated_ffn_workspace_bytes(B, dim, F) bytes, caller-owned,
+ * 16-byte aligned; it holds nothing between calls.
+ *
+ * pkm_gated_ffn_backward: from the forward's x, weights, gate and up, and dy
+ * [B, dim] bf16 (the gradient of y):
+ *   dh = dy Wd,  dg = dh * u * act'(g),  du = dh * act(g)
+ *   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h
+ * dx [B, dim] bf16, overwritten; dw_gate, dw_up [F, dim] and dw_down [dim, F]:
+ * grad_dtype PKM_BF16: overwritten, rounded once; PKM_F32: fp32, added to (zero
+ * them first, or accumulate over several batches).  dx may be NULL, dw_gate
+ * and dw_up may be NULL together, dw_down may be NULL: those gradients are
+ * not computed.  dg, du and h are kept in bf16 in the workspace
+ * (pkm_gated_ffn_backward_workspace_bytes).
+ *
+ * B == 0 is a no-op, except that bf16 weight gradients are set to zero.
+ * status: as pkm_query_net's.  Errors: PKM_ERR_INVALID (NULL pointer, B < 0,
+ * dim < 1, F < 1, one of two that go together), PKM_ERR_UNSUPPORTED (dim or F
+ * no multiple of 8, act, grad_dtype), PKM_ERR_RANGE (a product's tiles above
+ * 2^31 - 1), PKM_ERR_ALIGN (a pointer not 16-byte aligned), PKM_ERR_CUDA.
+ */
+enum {
+  PKM_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+  PKM_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+  PKM_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+  PKM_ACT_RELU = 3       /* max(g, 0), slope 0 at 0 */
+};
+size_t pkm_gated_ffn_workspace_bytes(int B, int dim, int F);
+int pkm_gated_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, int B,
+                  int dim, int F, int act, void *workspace, void *y, void *gate, void *up,
+                  int *status, void *stream);
+size_t pkm_gated_ffn_backward_workspace_bytes(int B, int dim, int F);
+int pkm_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up,
+                           const void *w_down, const void *gate, const void *up, const void *dy,
+                           int B, int dim, int F, int act, void *workspace, void *dx,
+                           void *dw_gate, void *dw_up, void *dw_down, int grad_dtype, int *status,
+                           void *stream);
+
+/*
+ * Distillation from a teacher's top logits: the loss that brings a model back
+ * after some of its blocks were replaced by memories, from lists in the layout
+ * a lookup returns.  Per row b, with student logits z [V], the teacher's list
+ * idx, teacher [k] and a temperature T > 0:
+ *
+ *   p = softmax(teacher / T) over the list,  q = softmax(z / T) over all V
+ *   loss[b] = T^2 sum_j p_j (log p_j - log q[idx_j])
+ *   lse[b]  = log sum_v exp(z_v / T)
+ *   dlogits = dloss[b] T (P q - sum_j p_j at idx_j),  P = sum_j p_j
+ *
+ * logits: [B, V] with ld elements from one row to the next (ld >= V), PKM_BF16
+ * or PKM_F32 (logit_dtype); idx [B, k] int64, teacher [B, k] fp32; loss, lse,
+ * dloss [B] fp32; dlogits: [B, V] of logit_dtype, ld_d elements from row to
+ * row (what lies between rows is left as it is).  logits and dlogits may start
+ * at any element and have any stride (16-byte aligned rows are fastest).
+ *
+ * An entry of a list with a negative idx, or a teacher logit of -inf, is
+ * absent; an idx >= V is absent too and sets *status to PKM_ERR_BAD_INDEX.  A
+ * row with no entry (a padding token) has loss 0 and a zero gradient.  A row
+ * whose dloss is 0 has a zero gradient whatever its logits hold.  A column
+ * that occurs twice counts twice.  Logits of -inf (masked columns) have q = 0;
+ * a list that names such a column with p > 0 has an infinite loss.  k up to
+ * PKM_DISTILL_MAX_K.
+ *
+ * pkm_distill: loss, and lse unless NULL.  pkm_distill_backward: dlogits from
+ * the forward's lse and the loss's gradient dloss.  pkm_distill_train: all
+ * three in one call, for a training step that knows dloss beforehand (1 / B
+ * for a mean).  dlogits may be logits itself (then ld_d == ld), so a step needs one
+ * [B, V] matrix.  status: NULL, or a device int that receives
+ * PKM_ERR_BAD_INDEX (it is not cleared).  Errors: PKM_ERR_INVALID (NULL
+ * pointer, B < 0, V < 1, k < 1, T not positive and finite), PKM_ERR_UNSUPPORTED
+ * (logit_dtype, k), PKM_ERR_RANGE (ld or ld_d below V; in place with two
+ * strides), PKM_ERR_ALIGN (a pointer inside an element), PKM_ERR_CUDA.
+ * B == 0 is a no-op.
+ */
+#define PKM_DISTILL_MAX_K 512
+int pkm_distill(const void *logits, int logit_dtype, int64_t ld, int B, int V, const int64_t *idx,
+                const float *teacher, int k, float temperature, float *loss, float *lse,
+                int *status, void *stream);
+int pkm_distill_backward(const void *logits, int logit_dtype, int64_t ld, int B, int V,
+                         const int64_t *idx, const float *teacher, int k, float temperature,
+                         const float *lse, const float *dloss, void *dlogits, int64_t ld_d,
+                         int *status, void *stream);
+int pkm_distill_train(const void *logits, int logit_dtype, int64_t ld, int B, int V,
+                      const int64_t *idx, const float *teacher, int k, float temperature,
+                      const float *dloss, float *loss, float *lse, void *dlogits, int64_t ld_d,
+                      int *status, void *stream);
 
 #ifdef __cplusplus
 }

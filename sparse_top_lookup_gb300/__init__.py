@@ -22,6 +22,8 @@ PKM_OPT_HINT_Z, PKM_OPT_HOST_CHUNKS, PKM_OPT_TEST_STALL = 1, 2, 3
 PKM_OPT_READ_SMS = 4
 PKM_OPT_SELECT_FORM = 5
 PKM_HOST_MAX_CHUNKS = 16
+PKM_ACT_SILU, PKM_ACT_GELU, PKM_ACT_GELU_TANH, PKM_ACT_RELU = 0, 1, 2, 3
+PKM_DISTILL_MAX_K = 512
 
 EXPORTED = ["pkm_create", "pkm_destroy", "pkm_forward", "pkm_lookup", "pkm_gather",
             "pkm_forward_host", "pkm_get_status", "pkm_check_args", "pkm_strerror",
@@ -29,7 +31,10 @@ EXPORTED = ["pkm_create", "pkm_destroy", "pkm_forward", "pkm_lookup", "pkm_gathe
             "pkm_quantize_values_fp8", "pkm_bn_fold", "pkm_query_net", "pkm_backward", "pkm_backward_read",
             "pkm_backward_scores", "pkm_forward_host_async", "pkm_backward_sparse",
             "pkm_backward_read_sparse", "pkm_multicast_ok", "pkm_full_keys", "pkm_flat_lookup",
-            "pkm_query_net_batch", "pkm_query_net_batch_workspace_bytes"]
+            "pkm_query_net_batch", "pkm_query_net_batch_workspace_bytes",
+            "pkm_gated_ffn", "pkm_gated_ffn_workspace_bytes", "pkm_gated_ffn_backward",
+            "pkm_gated_ffn_backward_workspace_bytes", "pkm_distill", "pkm_distill_backward",
+            "pkm_distill_train"]
 PKM_STATIC_MAX_PAIRS = 1 << 16
 
 
@@ -96,13 +101,25 @@ def lib():
         L.pkm_flat_lookup.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
         L.pkm_backward_read_sparse.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp,
                                                vp, vp, vp]
+        f32, i64 = ctypes.c_float, ctypes.c_int64
+        L.pkm_gated_ffn.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.pkm_gated_ffn_backward.argtypes = [vp] * 7 + [i32] * 4 + [vp] * 5 + [i32, vp, vp]
+        for f in ("pkm_gated_ffn_workspace_bytes", "pkm_gated_ffn_backward_workspace_bytes"):
+            getattr(L, f).argtypes = [i32, i32, i32]
+            getattr(L, f).restype = ctypes.c_size_t
+        L.pkm_distill.argtypes = [vp, i32, i64, i32, i32, vp, vp, i32, f32, vp, vp, vp, vp]
+        L.pkm_distill_backward.argtypes = [vp, i32, i64, i32, i32, vp, vp, i32, f32, vp, vp, vp,
+                                           i64, vp, vp]
+        L.pkm_distill_train.argtypes = [vp, i32, i64, i32, i32, vp, vp, i32, f32, vp, vp, vp, vp,
+                                        i64, vp, vp]
         for f in ("pkm_create", "pkm_forward", "pkm_lookup", "pkm_gather", "pkm_forward_host",
                   "pkm_get_status", "pkm_check_args", "pkm_abi_version", "pkm_set_option",
                   "pkm_get_fallback_count", "pkm_lookup_static", "pkm_quantize_values_fp8",
                   "pkm_bn_fold", "pkm_query_net", "pkm_backward", "pkm_backward_read",
                   "pkm_backward_scores", "pkm_forward_host_async", "pkm_backward_sparse",
                   "pkm_backward_read_sparse", "pkm_full_keys", "pkm_flat_lookup",
-                  "pkm_query_net_batch"):
+                  "pkm_query_net_batch", "pkm_gated_ffn", "pkm_gated_ffn_backward", "pkm_distill",
+                  "pkm_distill_backward", "pkm_distill_train"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -297,6 +314,82 @@ def pkm_query_net(x, weight, B, dim, F, scale, shift, q, status=None, stream=Non
     """q = (x W^T) * scale + shift in bf16: the query network ahead of the lookup."""
     return lib().pkm_query_net(_addr(x), _addr(weight), B, dim, F, _addr(scale), _addr(shift),
                                _addr(q), _addr(status), _stream(stream))
+
+
+def _dense(x, where):
+    """x's address, for an argument that has to be contiguous (tensors and arrays are checked)."""
+    flags = getattr(x, "flags", None)
+    if (x.is_contiguous() if hasattr(x, "is_contiguous") else
+            flags is None or flags["C_CONTIGUOUS"]):
+        return _addr(x)
+    raise ValueError("%s: arguments are contiguous: got strides %r" % (where, x.stride()
+                     if hasattr(x, "stride") else x.strides))
+
+
+def _rows(x, ld, where):
+    """x's address, for a matrix whose rows are contiguous and ld elements apart."""
+    if hasattr(x, "stride") and x.dim() == 2 and (
+            (x.size(1) > 1 and x.stride(1) != 1) or (x.size(0) > 1 and x.stride(0) != ld)):
+        raise ValueError("%s: rows are contiguous and ld elements apart: got strides %r, ld %d"
+                         % (where, tuple(x.stride()), ld))
+    return _addr(x)
+
+
+def pkm_gated_ffn_workspace_bytes(B, dim, F):
+    return int(lib().pkm_gated_ffn_workspace_bytes(B, dim, F))
+
+
+def pkm_gated_ffn(x, w_gate, w_up, w_down, B, dim, F, act, workspace, y, gate=None, up=None,
+                  status=None, stream=None):
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T in bf16; gate and up keep the two projections
+    for the backward pass (see include/pkm.h)."""
+    a = [_dense(t, "pkm_gated_ffn") for t in (x, w_gate, w_up, w_down, workspace, y, gate, up)]
+    return lib().pkm_gated_ffn(*a[:4], B, dim, F, act, *a[4:], _addr(status), _stream(stream))
+
+
+def pkm_gated_ffn_backward_workspace_bytes(B, dim, F):
+    return int(lib().pkm_gated_ffn_backward_workspace_bytes(B, dim, F))
+
+
+def pkm_gated_ffn_backward(x, w_gate, w_up, w_down, gate, up, dy, B, dim, F, act, workspace, dx,
+                           dw_gate, dw_up, dw_down, grad_dtype=PKM_BF16, status=None, stream=None):
+    """Gradients of pkm_gated_ffn: dx overwritten; the weights' overwritten in bf16, or added to
+    in fp32 (grad_dtype PKM_F32); any of dx, (dw_gate, dw_up) and dw_down may be None."""
+    a = [_dense(t, "pkm_gated_ffn_backward") for t in
+         (x, w_gate, w_up, w_down, gate, up, dy, workspace, dx, dw_gate, dw_up, dw_down)]
+    return lib().pkm_gated_ffn_backward(*a[:7], B, dim, F, act, *a[7:], grad_dtype, _addr(status),
+                                        _stream(stream))
+
+
+def pkm_distill(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature, loss, lse=None,
+                status=None, stream=None):
+    """The loss of student logits [B, V] (rows ld apart) against a teacher's lists idx, teacher
+    [B, k], and the rows' log-sum-exp (see include/pkm.h)."""
+    w = "pkm_distill"
+    return lib().pkm_distill(_rows(logits, ld, w), logit_dtype, ld, B, V, _dense(idx, w),
+                             _dense(teacher, w), k, float(temperature), _dense(loss, w),
+                             _dense(lse, w), _addr(status), _stream(stream))
+
+
+def pkm_distill_backward(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature, lse, dloss,
+                         dlogits, ld_d, status=None, stream=None):
+    """dlogits from the loss's gradient dloss [B] and the forward's lse; dlogits may be logits."""
+    w = "pkm_distill_backward"
+    return lib().pkm_distill_backward(_rows(logits, ld, w), logit_dtype, ld, B, V, _dense(idx, w),
+                                      _dense(teacher, w), k, float(temperature), _dense(lse, w),
+                                      _dense(dloss, w), _rows(dlogits, ld_d, w), ld_d,
+                                      _addr(status), _stream(stream))
+
+
+def pkm_distill_train(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature, dloss, loss,
+                      lse, dlogits, ld_d, status=None, stream=None):
+    """loss, lse and dlogits in one call, for a dloss [B] known beforehand; dlogits may be
+    logits."""
+    w = "pkm_distill_train"
+    return lib().pkm_distill_train(_rows(logits, ld, w), logit_dtype, ld, B, V, _dense(idx, w),
+                                   _dense(teacher, w), k, float(temperature), _dense(dloss, w),
+                                   _dense(loss, w), _dense(lse, w), _rows(dlogits, ld_d, w), ld_d,
+                                   _addr(status), _stream(stream))
 
 
 def fp8_table_bytes(N, d_v):

@@ -154,6 +154,30 @@ cudaError_t launch_merge(const float* list_v, const unsigned short* list_c, int 
 // The hint_z launch_lookup_tc uses unless a handle overrides it.
 float default_hint_z(int n_keys, int k);
 
+// The gated feed-forward block and its backward pass (ffn.cu); arguments as
+// pkm_gated_ffn's and pkm_gated_ffn_backward's, checked.
+size_t gated_ffn_workspace_bytes(int B, int F);
+size_t gated_ffn_backward_workspace_bytes(int B, int F);
+cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up,
+                             const void* w_down, int B, int dim, int F, int act, void* workspace,
+                             void* y, void* gate, void* up, int* status, cudaStream_t stream);
+cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up,
+                                      const void* w_down, const void* gate, const void* up,
+                                      const void* dy, int B, int dim, int F, int act,
+                                      void* workspace, void* dx, void* dw_gate, void* dw_up,
+                                      void* dw_down, int grad_dtype, int* status,
+                                      cudaStream_t stream);
+
+// Distillation from a teacher's top logits (distill.cu); arguments as
+// pkm_distill's and pkm_distill_backward's, checked.
+cudaError_t launch_distill(const void* z, int dtype, int64_t ld, int B, int V, const int64_t* idx,
+                           const float* teacher, int k, float T, float* loss, float* lse,
+                           int* status, cudaStream_t stream);
+cudaError_t launch_distill_backward(const void* z, int dtype, int64_t ld, int B, int V,
+                                    const int64_t* idx, const float* teacher, int k, float T,
+                                    const float* lse, const float* dloss, void* dz, int64_t ld_d,
+                                    int* status, cudaStream_t stream);
+
 // Limits of each path (checked on the host before a launch).
 constexpr int kSimtMaxK = 64;
 constexpr int kSimtMaxNKeys = 4096;

@@ -302,6 +302,22 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
          ((uint32_t)(M >> 4) << 24);
 }
 
+// The same for an operand stored with M (N) contiguous (MN-major): K rows of
+// 128 bytes (64 elements of M or N), 8-row swizzle atoms 1024 bytes apart;
+// the next 64 elements of M or N begin `block` bytes further on.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t block) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(block >> 4) << 16;  // leading byte offset: next 64 of M (N)
+  d |= (uint64_t)(1024 >> 4) << 32;   // stride byte offset: next 8 of K
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Instruction-descriptor bits: A (B) is MN-major.
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
+
 // ------------------------------------------------------- bounded waits
 
 struct Ctl {
