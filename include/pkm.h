@@ -515,7 +515,10 @@ int pkm_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up,
  * whose dloss is 0 has a zero gradient whatever its logits hold.  A column
  * that occurs twice counts twice.  Logits of -inf (masked columns) have q = 0;
  * a list that names such a column with p > 0 has an infinite loss.  k up to
- * PKM_DISTILL_MAX_K.
+ * PKM_DISTILL_MAX_K.  lse is fp32: where a row's logits are all so far from zero
+ * (10^5 T and more, as when every one is a mask of a large negative value) that lse cannot hold
+ * log V beside them, pkm_distill_backward's q is no better than that, while
+ * pkm_distill_train's is exact.
  *
  * pkm_distill: loss, and lse unless NULL.  pkm_distill_backward: dlogits from
  * the forward's lse and the loss's gradient dloss.  pkm_distill_train: all
@@ -523,7 +526,7 @@ int pkm_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up,
  * for a mean).  dlogits may be logits itself (then ld_d == ld), so a step needs one
  * [B, V] matrix.  status: NULL, or a device int that receives
  * PKM_ERR_BAD_INDEX (it is not cleared).  Errors: PKM_ERR_INVALID (NULL
- * pointer, B < 0, V < 1, k < 1, T not positive and finite), PKM_ERR_UNSUPPORTED
+ * pointer, B < 0, V < 1, k < 1, T not finite or below 1e-30), PKM_ERR_UNSUPPORTED
  * (logit_dtype, k), PKM_ERR_RANGE (ld or ld_d below V; in place with two
  * strides), PKM_ERR_ALIGN (a pointer inside an element), PKM_ERR_CUDA.
  * B == 0 is a no-op.

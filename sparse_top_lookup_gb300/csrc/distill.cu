@@ -7,22 +7,102 @@
 //   dz   = dloss * T * (P q - sum_j p_j [idx_j])      P = sum_j p_j (1, or 0
 //                                                     for an empty list)
 // An entry with a negative idx, or a t of -inf, is absent.
+//
+// Bound by HBM: the logits are read once and (with a gradient) dz is written
+// once.  A row is held in shared memory between its sum and its gradient.  It
+// is cut into slices, one for each CTA of a cluster, which exchange (maximum,
+// sum); short rows are held in the registers of a warp each.
+//
+// Softmax arithmetic is in powers of two: with c = log2(e) / T and the
+// largest logit m, the terms are 2^((z - m) c).  The difference comes first:
+// logits at the type's lowest value, as some masks have them, would overflow
+// in z c.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "pkm_internal.cuh"
+#include "tc_common.cuh"
 
 namespace pkm {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int DTHREADS = 512;
+using tc::cluster_ctarank;
+using tc::mapa_shared;
+using tc::smem_u32;
 
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int DTHREADS = 256;
+constexpr int DWARPS = DTHREADS / 32;
+constexpr int kMaxLsh = 3, kMaxSlices = 1 << kMaxLsh;  // CTAs of a cluster (the portable limit)
+constexpr int kWarpMaxK = 128;   // longest list of the warp-per-row form (its shared memory)
+
+enum Mode { kFwd, kBwd, kTrain };
+
+template <typename E>
+struct El;
+template <>
+struct El<float> {
+  static constexpr int kPerVec = 4;
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  __device__ static float get(float v) { return v; }
+  __device__ static void put(float* p, float v) { *p = v; }
+  __device__ static float get(const uint4& d, int i) {
+    return __uint_as_float(i == 0 ? d.x : i == 1 ? d.y : i == 2 ? d.z : d.w);
+  }
+  __device__ static float vmax(const uint4& d) {
+    return fmaxf(fmaxf(get(d, 0), get(d, 1)), fmaxf(get(d, 2), get(d, 3)));
+  }
+};
+template <>
+struct El<__nv_bfloat16> {
+  static constexpr int kPerVec = 8;
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+  __device__ static float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  __device__ static void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+  __device__ static float get(const uint4& d, int i) {
+    const uint32_t w = i < 2 ? d.x : i < 4 ? d.y : i < 6 ? d.z : d.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+  __device__ static float vmax(const uint4& d) {
+    auto h = [](const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(h(d.x), h(d.y)), __hmax2(h(d.z), h(d.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&w);
+}
+
+// Two fp32 values in one register pair, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // log of a positive s as a double good to about 1e-8: the exponent's part
 // exactly, the mantissa's (a value in [0.75, 1.5)) by logf.
@@ -36,20 +116,100 @@ __device__ __forceinline__ double log_split(float s) {
   return (double)e * 0.6931471805599453 + (double)logf(f);
 }
 
-struct ListStats {
-  float tm;     // largest t of the present entries, -inf if none is present
-  float total;  // sum of exp((t - tm) / T)
+// s * exp(m / T), s in the order of 1 (m = -inf: nothing yet, s is 0 or NaN).
+struct Sum {
+  float m, s;
+};
+// The sum over the first kLanes lanes of a warp (a power of two), on every one of them.
+template <int kLanes>
+__device__ __forceinline__ Sum lanes_join(Sum a, float c) {
+  float m = a.m;
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = m == -INFINITY ? a.s : a.s * ex2((a.m - m) * c);
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return Sum{m, s};
+}
+
+struct DistillArgs {
+  const void* z;
+  void* dz;
+  int64_t ld, ld_d;
+  int B, V, k, kpad;  // kpad: k rounded up to 4
+  int lsh;            // log2 of a row's slices: the cluster's CTAs, or (kBwd) separate units
+  int slots, chunk;   // ring of the CTA-per-slice form: slots of `chunk` 16-byte vectors
+  float T;
+  const int64_t* idx;
+  const float *teacher, *dloss;
+  float *loss, *lse;  // kBwd reads lse
+  int* status;
 };
 
-// By one whole warp.  An idx >= V counts as absent and is reported.
-__device__ ListStats list_stats(const int64_t* __restrict__ idx, const float* __restrict__ t,
-                                int k, int V, float c, int lane, int* status) {
+// A row as whole 16-byte vectors, and the few elements before and after them (slice 0's); the
+// vectors [v0, v1) are one slice's.
+template <typename E>
+struct Row {
+  const E* z;
+  const uint4* vec;
+  int head, nvec, v0, v1, extra;  // extra: this thread's element outside the vectors, or -1
+  __device__ Row(const DistillArgs& a, int64_t b, int slice, int lsh, int tid) {
+    constexpr int kPer = El<E>::kPerVec;
+    z = static_cast<const E*>(a.z) + b * a.ld;
+    const int off = (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(E));
+    head = min((kPer - off) % kPer, a.V);
+    nvec = (a.V - head) / kPer;
+    vec = reinterpret_cast<const uint4*>(z + head);
+    const int per = (nvec + (1 << lsh) - 1) >> lsh;
+    v0 = min(slice * per, nvec), v1 = min(v0 + per, nvec);
+    extra = slice == 0 && tid < a.V - nvec * kPer ? (tid < head ? tid : nvec * kPer + tid) : -1;
+  }
+  // whether column `at` is this slice's
+  __device__ bool mine(int at, int slice) const {
+    constexpr int kPer = El<E>::kPerVec;
+    if (at < head || at >= head + nvec * kPer) return slice == 0;
+    const int v = (at - head) / kPer;
+    return v >= v0 && v < v1;
+  }
+};
+
+// The teacher's list of one row in shared memory.
+struct List {
+  int* idx;    // column, -1: absent
+  float* t;
+  float* z;    // the student's logit there
+  float* p;    // softmax over the list (0 where absent)
+  float* dz;   // the column's gradient
+  __device__ List(unsigned char* base, int kpad)
+      : idx(reinterpret_cast<int*>(base)),
+        t(reinterpret_cast<float*>(base) + kpad),
+        z(reinterpret_cast<float*>(base) + 2 * kpad),
+        p(reinterpret_cast<float*>(base) + 3 * kpad),
+        dz(reinterpret_cast<float*>(base) + 4 * kpad) {}
+};
+constexpr int kListBytes = 20;  // per entry
+
+// By one warp: loads the list of row b and forms p.  Returns the largest t (-inf for an
+// empty list) and the sum of exp((t - largest) / T).
+template <typename E>
+__device__ Sum load_list(const List& l, const DistillArgs& a, int64_t b, float c, int lane,
+                         bool report) {
+  const E* row = static_cast<const E*>(a.z) + b * a.ld;
   float tm = -INFINITY;
-  for (int j = lane; j < k; j += 32) {
-    const int64_t i = idx[j];
-    if (i >= V) atomicExch(status, PKM_ERR_BAD_INDEX);
-    const float v = t[j];
-    if (i >= 0 && i < V) tm = v > tm || isnan(v) ? v : tm;
+  for (int j = lane; j < a.kpad; j += 32) {
+    int at = -1;
+    float t = -INFINITY, zj = 0.0f;
+    if (j < a.k) {
+      const int64_t i = a.idx[b * a.k + j];
+      t = a.teacher[b * a.k + j];
+      if (i >= a.V && report) atomicExch(a.status, PKM_ERR_BAD_INDEX);
+      if (i >= 0 && i < a.V && t != -INFINITY) {
+        at = (int)i;
+        zj = El<E>::get(row[i]);
+        tm = t > tm || isnan(t) ? t : tm;
+      }
+    }
+    l.idx[j] = at, l.t[j] = t, l.z[j] = zj;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -57,125 +217,567 @@ __device__ ListStats list_stats(const int64_t* __restrict__ idx, const float* __
     tm = v > tm || isnan(v) ? v : tm;
   }
   float total = 0.0f;
-  if (tm != -INFINITY)
-    for (int j = lane; j < k; j += 32)
-      if (idx[j] >= 0 && idx[j] < V) total += exp2f((t[j] - tm) * c);
+  for (int j = lane; j < a.kpad; j += 32) {
+    const float e = l.idx[j] >= 0 ? ex2((l.t[j] - tm) * c) : 0.0f;
+    l.p[j] = e;
+    total += e;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return ListStats{tm, total};
+  const float inv = total > 0.0f || isnan(total) ? 1.0f / total : 0.0f;
+  for (int j = lane; j < a.kpad; j += 32) l.p[j] *= inv;
+  return Sum{tm, total};
 }
 
-// loss and lse: one CTA per row.
-template <typename E>
-__global__ void __launch_bounds__(DTHREADS)
-distill_forward_kernel(const E* __restrict__ z, int64_t ld, int V, const int64_t* __restrict__ idx,
-                       const float* __restrict__ teacher, int k, float T, float* __restrict__ loss,
-                       float* __restrict__ lse, int* __restrict__ status) {
-  __shared__ float s_m[DTHREADS / 32], s_s[DTHREADS / 32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = blockIdx.x;
-  const float c = kLog2e / T;
-  const E* row = z + b * ld;
-  float m = -INFINITY, s = 0.0f;
-  for (int v = threadIdx.x; v < V; v += DTHREADS) {
-    const float x = to_f(row[v]);
-    if (x > m) {
-      s *= exp2f((m - x) * c);
-      m = x;
-    }
-    s += x == -INFINITY ? 0.0f : exp2f((x - m) * c);
-  }
-  auto join = [&](float m2, float s2) {
-    const float mm = fmaxf(m, m2);
-    if (mm != -INFINITY) {
-      s = s * exp2f((m - mm) * c) + s2 * exp2f((m2 - mm) * c);
-      m = mm;
-    } else {
-      s += s2;
-    }
-  };
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m2, s2);
-  }
-  if (lane == 0) s_m[warp] = m, s_s[warp] = s;
-  __syncthreads();
-  if (warp) return;
-  m = lane < DTHREADS / 32 ? s_m[lane] : -INFINITY;
-  s = lane < DTHREADS / 32 ? s_s[lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m2, s2);
-  }
-  const double inv_t = 1.0 / (double)T;
-  const double L = s == 0.0f ? -INFINITY : m * inv_t + log_split(s);
-  idx += b * k, teacher += b * k;
-  const ListStats st = list_stats(idx, teacher, k, V, c, lane, status);
-  double sum = 0.0;
-  if (st.tm != -INFINITY) {
-    const double off = L - st.tm * inv_t - log_split(st.total);
-    for (int j = lane; j < k; j += 32) {
-      const int64_t i = idx[j];
-      if (i < 0 || i >= V) continue;
-      const float p = exp2f((teacher[j] - st.tm) * c) / st.total;
-      const float x = to_f(row[i]);
-      if (p != 0.0f)
-        sum += x == -INFINITY ? INFINITY : p * (((double)teacher[j] - x) * inv_t + off);
+// By one warp: loss and lse of row b from its sum and its list (ls: what load_list returned).
+// The loss is a small difference of its terms: those are in 64 bits.
+__device__ void put_loss(const DistillArgs& a, int64_t b, const Sum& sum, const List& list,
+                         const Sum& ls, int lane) {
+  const double inv_t = 1.0 / (double)a.T;
+  const double L = sum.s == 0.0f ? -INFINITY
+                                 : (sum.m == -INFINITY ? 0.0f : sum.m) * inv_t + log_split(sum.s);
+  double terms = 0.0;
+  if (ls.m != -INFINITY) {
+    const double o = L - ls.m * inv_t - log_split(ls.s);
+    for (int j = lane; j < a.k; j += 32) {
+      const float p = list.p[j];
+      if (p != 0.0f)  // (a NaN counts)
+        terms += list.z[j] == -INFINITY ? INFINITY
+                                        : p * (((double)list.t[j] - list.z[j]) * inv_t + o);
     }
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int o = 16; o; o >>= 1) terms += __shfl_xor_sync(0xffffffffu, terms, o);
   if (lane == 0) {
-    loss[b] = (float)(sum * (double)T * T);
-    if (lse) lse[b] = (float)L;
+    a.loss[b] = (float)(terms * (double)a.T * a.T);
+    if (a.lse) a.lse[b] = (float)L;
   }
 }
 
-// dz: one CTA per row.
-template <typename E>
-__global__ void __launch_bounds__(DTHREADS)
-distill_backward_kernel(const E* z, int64_t ld, int V, const int64_t* __restrict__ idx,
-                        const float* __restrict__ teacher, int k, float T,
-                        const float* __restrict__ lse, const float* __restrict__ dloss, E* dz,
-                        int64_t ld_d, int* __restrict__ status) {
-  __shared__ ListStats s_st;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = blockIdx.x;
-  const float c = kLog2e / T, g = dloss[b] * T;
-  const E* row = z + b * ld;
-  E* out = dz + b * ld_d;
-  idx += b * k, teacher += b * k;
-  if (warp == 0) {
-    const ListStats st = list_stats(idx, teacher, k, V, c, lane, status);
-    if (lane == 0) s_st = st;
+// g q(z) of a row.  In the training form from the row's sum; every q is 0 when every logit is
+// -inf.  In the backward form from an lse in fp32: a quarter of the exponent at a time (no
+// overflow), and never above 0.
+template <bool kFromLse>
+struct Grad {
+  float c, ref, scale;
+  __device__ float operator()(float z) const {
+    if constexpr (kFromLse) return ex2(fminf(4.0f * fmaf(z, 0.25f * c, -ref), 0.0f)) * scale;
+    return ex2((z - ref) * c) * scale;
   }
-  __syncthreads();
-  const ListStats st = s_st;
-  if (g == 0.0f || st.tm == -INFINITY) {
-    for (int v = threadIdx.x; v < V; v += DTHREADS) put(out + v, 0.0f);
+  __device__ float2 two(float z0, float z1) const {
+    if constexpr (kFromLse) return make_float2((*this)(z0), (*this)(z1));
+    const float2 e = unpair(mul2(add2(pair(z0, z1), pair(-ref, -ref)), pair(c, c)));
+    return unpair(mul2(pair(ex2(e.x), ex2(e.y)), pair(scale, scale)));
+  }
+};
+__device__ __forceinline__ Grad<false> grad_of(const Sum& sum, float g, float c) {
+  return {c, sum.m == -INFINITY ? 0.0f : sum.m, sum.s == 0.0f ? 0.0f : __fdividef(g, sum.s)};
+}
+__device__ __forceinline__ Grad<true> grad_of(float lse, float g, float c) {
+  // (a row whose lse is NaN or +inf has no gradient)
+  return {c, lse == -INFINITY ? 0.0f : lse * 0.25f * kLog2e, lse < INFINITY ? g : NAN};
+}
+
+// By `threads` threads: the gradients of the listed columns, from z as it was (dz may be z).
+template <typename G>
+__device__ void list_grad(const List& list, const DistillArgs& a, const G& q, float g, int tid,
+                          int threads) {
+  for (int j = tid; j < a.k; j += threads) {
+    const int at = list.idx[j];
+    if (at < 0) continue;
+    float p = 0.0f;  // of every entry that names this column
+    for (int l = 0; l < a.kpad; l += 4) {
+      const int4 i4 = *reinterpret_cast<const int4*>(list.idx + l);
+      const float4 p4 = *reinterpret_cast<const float4*>(list.p + l);
+      p += (i4.x == at ? p4.x : 0.0f) + (i4.y == at ? p4.y : 0.0f) +
+           (i4.z == at ? p4.z : 0.0f) + (i4.w == at ? p4.w : 0.0f);
+    }
+    list.dz[j] = fmaf(-g, p, q(list.z[j]));
+  }
+}
+
+// One vector of dz per lane: vector v (< end) of the row's out + head, from z's vector d.  `same`:
+// the rows of z and dz start alike within 16 bytes.  Otherwise the warp's 32 vectors go
+// through `stage` and out as whole words (bf16: with single elements at the ends).
+template <typename E, typename G>
+__device__ __forceinline__ void put_vector(E* body, int v, int end, const uint4& d, const G& q,
+                                           bool zero, bool same, uint4* stage, int lane) {
+  constexpr int kPer = El<E>::kPerVec;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2) {
+    const float2 f = q.two(El<E>::get(d, i), El<E>::get(d, i + 1));
+    if constexpr (kPer == 8) {
+      w[i / 2] = zero ? 0u : pack2(f.x, f.y);
+    } else {
+      w[i] = zero ? 0u : __float_as_uint(f.x);
+      w[i + 1] = zero ? 0u : __float_as_uint(f.y);
+    }
+  }
+  if (same) {
+    if (v < end) __stcs(reinterpret_cast<uint4*>(body) + v, make_uint4(w[0], w[1], w[2], w[3]));
     return;
   }
-  const float L = lse[b] * kLog2e;
-  auto q = [&](float x) { return x == -INFINITY ? 0.0f : exp2f(fmaf(x, c, -L)); };
-  // the listed columns, kept until every thread is done with the row (dz may be z)
-  float keep = 0.0f;
-  for (int j0 = 0; j0 < k; j0 += DTHREADS) {
-    // (k <= DTHREADS: one round)
-    const int j = j0 + threadIdx.x;
-    if (j < k && idx[j] >= 0 && idx[j] < V) {
-      float p = 0.0f;  // every entry of this column
-      for (int l = 0; l < k; ++l)
-        if (idx[l] == idx[j]) p += exp2f((teacher[l] - st.tm) * c);
-      keep = g * (q(to_f(row[idx[j]])) - p / st.total);
+  const int first = v - lane;
+  const int n = min(32, end - first) * kPer;  // elements of the warp, may be <= 0
+  E* o = body + (int64_t)first * kPer;
+  stage[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+  __syncwarp();
+  const E* src = reinterpret_cast<const E*>(stage);
+  if constexpr (sizeof(E) == 4) {
+    for (int e = lane; e < n; e += 32) o[e] = src[e];
+  } else {
+    const int odd = (int)((reinterpret_cast<uintptr_t>(o) >> 1) & 1u);
+    for (int e = 2 * lane - odd; e < n; e += 64) {
+      if (e >= 0 && e + 1 < n)
+        *reinterpret_cast<__nv_bfloat162*>(o + e) = __nv_bfloat162(src[e], src[e + 1]);
+      else if (e >= 0)
+        o[e] = src[e];
+      else if (n > 0)
+        o[0] = src[0];
     }
   }
+  __syncwarp();
+}
+
+// sum joined with exp of vectors d, by one thread.
+template <typename E, int kNV>
+__device__ __forceinline__ void add_vectors(Sum& sum, const uint4 (&d)[kNV], float c) {
+  constexpr int kPer = El<E>::kPerVec;
+  float m = sum.m;
+#pragma unroll
+  for (int j = 0; j < kNV; ++j) m = fmaxf(m, El<E>::vmax(d[j]));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  const float before = m == -INFINITY ? sum.s : sum.s * ex2((sum.m - ref) * c);
+  const uint64_t minus = pair(-ref, -ref), cc = pair(c, c);
+  uint64_t s[2] = {pair(before, 0.0f), 0};
+#pragma unroll
+  for (int j = 0; j < kNV; ++j)
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      const float2 e =
+          unpair(mul2(add2(pair(El<E>::get(d[j], i), El<E>::get(d[j], i + 1)), minus), cc));
+      s[(i >> 1) & 1] = add2(s[(i >> 1) & 1], pair(ex2(e.x), ex2(e.y)));
+    }
+  const float2 t = unpair(add2(s[0], s[1]));
+  sum = Sum{m, t.x + t.y};
+}
+__device__ __forceinline__ void add_one(Sum& sum, float x, float c) {
+  const float m = fmaxf(sum.m, x);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  sum = Sum{m, (m == -INFINITY ? sum.s : sum.s * ex2((sum.m - ref) * c)) + ex2((x - ref) * c)};
+}
+
+template <typename E>
+__device__ __forceinline__ uint4 masked_vector() {
+  return make_uint4(El<E>::kNegInf, El<E>::kNegInf, El<E>::kNegInf, El<E>::kNegInf);
+}
+
+// kFwd and kTrain for short rows: a warp each, which keeps the row in registers, kNV vectors per
+// lane, between its sum and its gradient.
+template <typename E, int kNV, int kMode>
+__global__ void __launch_bounds__(DTHREADS)
+distill_warp_kernel(const DistillArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ uint4 s_stage[kMode == kFwd ? 1 : DTHREADS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float c = kLog2e / a.T;
+  const List list(smem + (size_t)warp * kListBytes * a.kpad, a.kpad);
+  for (int64_t b = (int64_t)blockIdx.x * DWARPS + warp; b < a.B; b += (int64_t)gridDim.x * DWARPS) {
+    const Row<E> row(a, b, 0, 0, lane);
+    uint4 d[kNV];
+#pragma unroll
+    for (int j = 0; j < kNV; ++j)
+      d[j] = j * 32 + lane < row.nvec ? __ldcs(row.vec + j * 32 + lane) : masked_vector<E>();
+    const float x = row.extra >= 0 ? El<E>::get(row.z[row.extra]) : -INFINITY;
+    const float g = kMode == kFwd ? 0.0f : a.dloss[b] * a.T;
+    const Sum ls = load_list<E>(list, a, b, c, lane, true);
+    Sum sum{-INFINITY, 0.0f};
+    add_vectors<E>(sum, d, c);
+    add_one(sum, x, c);
+    sum = lanes_join<32>(sum, c);
+    __syncwarp();
+    put_loss(a, b, sum, list, ls, lane);
+    if constexpr (kMode == kTrain) {
+      const bool zero = g == 0.0f || ls.m == -INFINITY;  // no gradient, whatever z holds
+      const Grad<false> q = grad_of(sum, g, c);
+      if (!zero) list_grad(list, a, q, g, lane, 32);
+      E* out = static_cast<E*>(a.dz) + b * a.ld_d;
+      const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
+#pragma unroll
+      for (int j = 0; j < kNV; ++j)
+        put_vector(out + row.head, j * 32 + lane, row.nvec, d[j], q, zero, same,
+                   s_stage + warp * 32, lane);
+      if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
+      __syncwarp();  // the listed columns' values replace those of the row
+      if (!zero)
+        for (int j = lane; j < a.k; j += 32)
+          if (list.idx[j] >= 0) El<E>::put(out + list.idx[j], list.dz[j]);
+    }
+    __syncwarp();
+  }
+}
+
+// kBwd: units of 8 vectors per thread, each by itself, in registers.
+constexpr int kBwdVecs = 8;
+template <typename E>
+__global__ void __launch_bounds__(DTHREADS, 4)
+distill_backward_kernel(const DistillArgs a) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ uint4 s_stage[DTHREADS];
+  __shared__ Sum s_ls;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c = kLog2e / a.T;
+  const List list(smem, a.kpad);
+  const int64_t units = (int64_t)a.B << a.lsh;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int64_t b = unit >> a.lsh;
+    const int slice = (int)(unit & ((1 << a.lsh) - 1));
+    const Row<E> row(a, b, slice, a.lsh, tid);
+    uint4 d[kBwdVecs];
+#pragma unroll
+    for (int j = 0; j < kBwdVecs; ++j) {
+      const int v = row.v0 + j * DTHREADS + tid;
+      d[j] = v < row.v1 ? __ldcs(row.vec + v) : masked_vector<E>();
+    }
+    const float x = row.extra >= 0 ? El<E>::get(row.z[row.extra]) : -INFINITY;
+    const float g = a.dloss[b] * a.T;
+    const Grad<true> q = grad_of(a.lse[b], g, c);
+    if (warp == 0) {
+      const Sum ls = load_list<E>(list, a, b, c, lane, slice == 0);
+      if (lane == 0) s_ls = ls;
+    }
+    __syncthreads();
+    const bool zero = g == 0.0f || s_ls.m == -INFINITY;
+    if (!zero) list_grad(list, a, q, g, tid, DTHREADS);
+    E* out = static_cast<E*>(a.dz) + b * a.ld_d;
+    const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
+#pragma unroll
+    for (int j = 0; j < kBwdVecs; ++j)
+      put_vector(out + row.head, row.v0 + j * DTHREADS + tid, row.v1, d[j], q, zero, same,
+                 s_stage + warp * 32, lane);
+    if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
+    __syncthreads();  // the listed columns' values replace those of the row
+    if (!zero)
+      for (int j = tid; j < a.k; j += DTHREADS) {
+        const int at = list.idx[j];
+        if (at >= 0 && row.mine(at, slice)) El<E>::put(out + at, list.dz[j]);
+      }
+    __syncthreads();  // the list and s_ls have been read
+  }
+}
+
+// kFwd and kTrain: a CTA per slice of a row, a cluster per row.
+//   warps 0..7  (data) each chunk of the slice: maximum and sum; the slice's sums are exchanged
+//               between the cluster's CTAs through shared memory (st.async); then (kTrain)
+//               each chunk again: the gradient, written out;
+//   warp 8      (list) the loss, and the next row's list;
+//   warp 9      (copies) the slices' chunks by bulk copies into a ring of slots.
+// In kTrain a slot is free when its gradient is written, and the ring holds two rows' slices: a
+// row is loaded while the one before it is worked on.
+constexpr int kStreamThreads = DTHREADS + 64;
+constexpr int kMaxSlots = 16;
+constexpr size_t kDynamic = 220 * 1024;  // dynamic shared memory at most
+constexpr int kTrainChunks = 12;  // of a slice, at most: they fit beside the longest lists
+constexpr int kChunkVecs = 4 * DTHREADS;  // 16 KB: 4 vectors per thread
+
+static_assert(kTrainChunks * 16 * kChunkVecs + 2 * kListBytes * PKM_DISTILL_MAX_K <= kDynamic,
+              "ring of the longest slices");
+
+template <typename E, int kMode>
+__global__ void __launch_bounds__(kStreamThreads, 3)
+distill_stream_kernel(const DistillArgs a) {
+  using namespace tc;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint4 s_stage[kMode == kFwd ? 1 : DTHREADS];
+  __shared__ Sum s_warp[2][DWARPS];
+  __shared__ __align__(8) Sum s_slice[2][kMaxSlices];
+  __shared__ Sum s_ls[2];
+  __shared__ __align__(8) uint64_t s_bars[2 * kMaxSlots + 2];
+  __shared__ int s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c = kLog2e / a.T;
+  const int lsh = a.lsh, slices = 1 << lsh;
+  const int slots = a.slots, chunk = a.chunk;
+  uint4* ring = reinterpret_cast<uint4*>(smem);
+  unsigned char* lists = smem + (size_t)slots * chunk * 16;
+  auto list_at = [&](int i) { return List(lists + (size_t)i * kListBytes * a.kpad, a.kpad); };
+  const uint32_t bar0 = smem_u32(s_bars);
+  auto bar_full = [&](int s) { return bar0 + 8u * s; };
+  auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxSlots + s); };
+  auto bar_sums = [&](int par) { return bar0 + 8u * (2 * kMaxSlots + par); };
+  if (tid == 0) {
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), DWARPS);
+    }
+    mbar_init(bar_sums(0), 1);
+    mbar_init(bar_sums(1), 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   __syncthreads();
-  for (int v = threadIdx.x; v < V; v += DTHREADS) put(out + v, g * q(to_f(row[v])));
-  __syncthreads();
-  if (threadIdx.x < k && idx[threadIdx.x] >= 0 && idx[threadIdx.x] < V)
-    put(out + idx[threadIdx.x], keep);
+  if (slices > 1) cluster_sync();  // every CTA's barriers exist before its memory is written
+  const Ctl ctl{&s_abort, a.status};
+
+  const int64_t units = (int64_t)a.B << lsh;
+  const int slice = (int)(blockIdx.x & (slices - 1));
+  // consecutive CTAs (a cluster's) take the slices of one row
+  if (warp == DWARPS + 1) {
+    // ---------------------------------------------------------------- copies
+    if (lane == 0) {
+      int s = 0, issued = 0;
+      uint32_t ph = 1;
+      bool ok = true;
+      for (int64_t unit = blockIdx.x; ok && unit < units; unit += gridDim.x) {
+        const Row<E> row(a, unit >> lsh, slice, lsh, 0);
+        for (int v = row.v0; v < row.v1; v += chunk) {
+          if (!(ok = wait_phase(bar_empty(s), ph, ctl))) break;
+          const uint32_t bytes = 16u * min(chunk, row.v1 - v);
+          mbar_expect_tx(bar_full(s), bytes);
+          bulk_load(smem_u32(ring + (size_t)s * chunk), row.vec + v, bytes, bar_full(s));
+          if (issued < slots) ++issued;
+          if (++s == slots) s = 0, ph ^= 1u;
+        }
+      }
+      // (normally the data warps have waited for them all) no copy outlives the CTA
+      for (int i = 0; i < issued; ++i) {
+        if (--s < 0) s = slots - 1, ph ^= 1u;
+        wait_phase_drain(bar_full(s), ph ^ 1u);
+      }
+    }
+    return;
+  }
+  // The list warp meets the data warps once a row, where the list is needed: it has the time of
+  // a row for the loss and the next row's list.  What it still reads then is kept twice (par).
+  const bool data = warp < DWARPS;
+  auto fetch = [&](int64_t unit, int par) {
+    if (unit >= units) return;
+    const Sum ls = load_list<E>(list_at(par), a, unit >> lsh, c, lane, slice == 0);
+    if (lane == 0) s_ls[par] = ls;
+  };
+  if (!data) fetch(blockIdx.x, 0);
+  int s1 = 0, s2 = 0;         // next slot of the first and the second pass
+  uint32_t ph = 0, sums = 0;  // its parity in the first; bit par: that of bar_sums(par)
+  float x_next = -INFINITY, g_next = 0.0f;
+  auto ahead = [&](int64_t unit) {  // what the row takes from memory besides the chunks
+    if (!data || unit >= units) return;
+    const Row<E> row(a, unit >> lsh, slice, lsh, tid);
+    x_next = row.extra >= 0 ? El<E>::get(row.z[row.extra]) : -INFINITY;
+    if (kMode == kTrain) g_next = a.dloss[unit >> lsh] * a.T;
+  };
+  ahead(blockIdx.x);
+  int par = 0;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, par ^= 1) {
+    const int64_t b = unit >> lsh;
+    const Row<E> row(a, b, slice, lsh, tid);
+    const List list = list_at(par);
+    const float x = x_next, g = g_next;
+    Sum sum{-INFINITY, 0.0f};
+    if (data) {
+      for (int v = row.v0; v < row.v1; v += chunk) {
+        wait_phase(bar_full(s1), ph, ctl);
+        const uint4* src = ring + (size_t)s1 * chunk;
+        const int n = min(chunk, row.v1 - v);
+        uint4 d[kChunkVecs / DTHREADS];
+#pragma unroll
+        for (int j = 0; j < kChunkVecs / DTHREADS; ++j)
+          d[j] = j * DTHREADS + tid < n ? src[j * DTHREADS + tid] : masked_vector<E>();
+        if constexpr (kMode == kFwd) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_empty(s1));
+        }
+        add_vectors<E>(sum, d, c);
+        if (++s1 == slots) s1 = 0, ph ^= 1u;
+      }
+      add_one(sum, x, c);
+      ahead(unit + gridDim.x);
+      sum = lanes_join<32>(sum, c);
+      if (lane == 0) s_warp[par][warp] = sum;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(DTHREADS + 32) : "memory");
+    sum = lanes_join<DWARPS>(s_warp[par][lane & (DWARPS - 1)], c);
+    if (slices > 1) {
+      // each CTA's sum to every CTA of the cluster, completing on the receiver's barrier.
+      // Two copies of s_slice: a CTA sends a row's sum after it has those of the row before,
+      // so after every other has read those of the row before that.
+      const uint32_t bar = bar_sums(par);
+      if (tid == 0) mbar_expect_tx(bar, 8u * slices);
+      if (tid < slices)
+        asm volatile(
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
+                "r"(mapa_shared(smem_u32(&s_slice[par][slice]), tid)),
+            "r"(__float_as_uint(sum.m)), "r"(__float_as_uint(sum.s)), "r"(mapa_shared(bar, tid))
+            : "memory");
+      wait_phase_cluster(bar, (sums >> par) & 1u, ctl);
+      sums ^= 1u << par;
+      __syncwarp();
+      sum = lanes_join<kMaxSlices>(lane % kMaxSlices < slices ? s_slice[par][lane % kMaxSlices]
+                                                              : Sum{-INFINITY, 0.0f}, c);
+    }
+    const Sum ls = s_ls[par];
+    if (!data) {
+      if (slice == 0) put_loss(a, b, sum, list, ls, lane);
+      fetch(unit + gridDim.x, par ^ 1);
+      continue;
+    }
+    if constexpr (kMode == kTrain) {
+      const bool zero = g == 0.0f || ls.m == -INFINITY;  // no gradient, whatever z holds
+      const Grad<false> q = grad_of(sum, g, c);
+      if (!zero) list_grad(list, a, q, g, tid, DTHREADS);
+      E* out = static_cast<E*>(a.dz) + b * a.ld_d;
+      const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
+      for (int v = row.v0; v < row.v1; v += chunk) {
+        const uint4* src = ring + (size_t)s2 * chunk;
+        const int n = min(chunk, row.v1 - v);
+#pragma unroll
+        for (int j = 0; j < kChunkVecs / DTHREADS; ++j) {
+          const int i = j * DTHREADS + tid;
+          if (i - lane >= n) break;
+          put_vector(out + row.head, v + i, v + n, i < n ? src[i] : masked_vector<E>(), q, zero,
+                     same, s_stage + warp * 32, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_empty(s2));
+        if (++s2 == slots) s2 = 0;
+      }
+      if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
+      // the listed columns' values replace those of the row
+      asm volatile("bar.sync 2, %0;" ::"n"(DTHREADS) : "memory");
+      if (!zero)
+        for (int j = tid; j < a.k; j += DTHREADS) {
+          const int at = list.idx[j];
+          if (at >= 0 && row.mine(at, slice)) El<E>::put(out + at, list.dz[j]);
+        }
+    }
+  }
+  // (a CTA leaves after its last row's wait: no other writes into its shared memory after that)
+}
+
+// CTAs that run at one time at most, for a grid that leaves no second round to a few.
+template <typename K>
+cudaError_t resident_ctas(int* out, K kernel, int threads, size_t smem) {
+  if (*out) return cudaSuccess;
+  int n = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
+  if (n < 1) return cudaErrorInvalidConfiguration;
+  *out = n * tc::sm_count();
+  return cudaSuccess;
+}
+
+template <typename E, int kNV, int kMode>
+cudaError_t launch_warps(const DistillArgs& a, cudaStream_t stream) {
+  static int most = 0;
+  auto kernel = distill_warp_kernel<E, kNV, kMode>;
+  cudaError_t e = resident_ctas(&most, kernel, DTHREADS, (size_t)DWARPS * kWarpMaxK * kListBytes);
+  if (e != cudaSuccess) return e;
+  const int ctas = (a.B + DWARPS - 1) / DWARPS;
+  kernel<<<ctas < most ? ctas : most, DTHREADS, (size_t)DWARPS * kListBytes * a.kpad, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename E>
+cudaError_t launch_backward(DistillArgs& a, cudaStream_t stream) {
+  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+  while (nvec > (int64_t)kBwdVecs * DTHREADS << a.lsh) ++a.lsh;
+  static int most = 0;
+  auto kernel = distill_backward_kernel<E>;
+  cudaError_t e =
+      resident_ctas(&most, kernel, DTHREADS, (size_t)PKM_DISTILL_MAX_K * kListBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)a.B << a.lsh;
+  kernel<<<(unsigned)(units < most ? units : most), DTHREADS, (size_t)kListBytes * a.kpad,
+           stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename E, int kMode>
+cudaError_t launch_stream(DistillArgs& a, cudaStream_t stream) {
+  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+  // slices of at most 32 KB; more and smaller ones while CTAs are few
+  while (a.lsh < kMaxLsh && nvec > (int64_t)2 * kChunkVecs << a.lsh) ++a.lsh;
+  while (a.lsh < kMaxLsh && ((int64_t)a.B << a.lsh) * 2 <= tc::sm_count() &&
+         nvec > 2 * DTHREADS << a.lsh)
+    ++a.lsh;
+  const int slices = 1 << a.lsh;
+  const int64_t per = (nvec + slices - 1) >> a.lsh;
+  // chunks of 1 KB steps up to 16 KB, and two slices of them in the ring (kFwd: four chunks)
+  a.chunk = per >= kChunkVecs ? kChunkVecs : (int)((per + 63) / 64 * 64);
+  if (a.chunk < 64) a.chunk = 64;
+  const int64_t chunks = (per + a.chunk - 1) / a.chunk;
+  const size_t lists = (size_t)2 * kListBytes * a.kpad;
+  const int64_t room = (kDynamic - lists) / ((size_t)a.chunk * 16);
+  a.slots = kMode == kFwd ? 4 : (int)(chunks * 2 < room ? chunks * 2 : room);
+  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+  if (a.slots < 1) a.slots = 1;  // (a row without vectors)
+  auto kernel = distill_stream_kernel<E, kMode>;
+  const size_t smem = (size_t)a.slots * a.chunk * 16 + lists;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = slices;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters that run at one time, by their size and shared memory (in steps of 4 KB)
+  constexpr size_t kStep = 4096;
+  static int most[kMaxLsh + 1][kDynamic / kStep + 1];
+  const size_t step = (smem + kStep - 1) / kStep;
+  int& n = most[a.lsh][step];
+  if (!n) {
+    static bool attr_set = false;
+    if (!attr_set) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kDynamic);
+      if (e != cudaSuccess) return e;
+      attr_set = true;
+    }
+    cfg.dynamicSmemBytes = step * kStep;
+    cfg.gridDim = dim3(slices * tc::sm_count());
+    int got = 0;
+    cudaError_t e = cudaOccupancyMaxActiveClusters(&got, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (got < 1) return cudaErrorInvalidConfiguration;
+    n = got;
+    cfg.dynamicSmemBytes = smem;
+  }
+  cfg.gridDim = dim3((unsigned)(a.B < n ? a.B : n) * slices);
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <typename E, int kMode>
+cudaError_t dispatch(DistillArgs& a, cudaStream_t stream) {
+  a.kpad = (a.k + 3) / 4 * 4;
+  a.lsh = 0;
+  if constexpr (kMode == kBwd) {
+    return launch_backward<E>(a, stream);
+  } else {
+    // rows of up to 4 KB, when there are enough of them to fill the GPU: a warp each
+    const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+    if (nvec <= 32 * 8 && a.k <= kWarpMaxK && a.B >= 4 * tc::sm_count())
+      return nvec <= 32 * 2 ? launch_warps<E, 2, kMode>(a, stream)
+                            : launch_warps<E, 8, kMode>(a, stream);
+    return launch_stream<E, kMode>(a, stream);
+  }
+}
+
+template <int kMode>
+cudaError_t dispatch_type(DistillArgs& a, int dtype, cudaStream_t stream) {
+  return dtype == PKM_BF16 ? dispatch<__nv_bfloat16, kMode>(a, stream)
+                           : dispatch<float, kMode>(a, stream);
+}
+
+DistillArgs args_of(const void* z, int64_t ld, int B, int V, const int64_t* idx,
+                    const float* teacher, int k, float T, int* status) {
+  DistillArgs a = {};
+  a.z = z, a.ld = ld, a.B = B, a.V = V, a.idx = idx, a.teacher = teacher, a.k = k, a.T = T;
+  a.status = status;
+  return a;
 }
 
 }  // namespace
@@ -183,28 +785,36 @@ distill_backward_kernel(const E* z, int64_t ld, int V, const int64_t* __restrict
 cudaError_t launch_distill(const void* z, int dtype, int64_t ld, int B, int V, const int64_t* idx,
                            const float* teacher, int k, float T, float* loss, float* lse,
                            int* status, cudaStream_t stream) {
-  if (dtype == PKM_BF16)
-    distill_forward_kernel<<<B, DTHREADS, 0, stream>>>(static_cast<const __nv_bfloat16*>(z), ld, V,
-                                                       idx, teacher, k, T, loss, lse, status);
-  else
-    distill_forward_kernel<<<B, DTHREADS, 0, stream>>>(static_cast<const float*>(z), ld, V, idx,
-                                                       teacher, k, T, loss, lse, status);
-  return cudaGetLastError();
+  DistillArgs a = args_of(z, ld, B, V, idx, teacher, k, T, status);
+  a.loss = loss, a.lse = lse;
+  return dispatch_type<kFwd>(a, dtype, stream);
 }
 
 cudaError_t launch_distill_backward(const void* z, int dtype, int64_t ld, int B, int V,
                                     const int64_t* idx, const float* teacher, int k, float T,
                                     const float* lse, const float* dloss, void* dz, int64_t ld_d,
                                     int* status, cudaStream_t stream) {
-  if (dtype == PKM_BF16)
-    distill_backward_kernel<<<B, DTHREADS, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(z), ld, V, idx, teacher, k, T, lse, dloss,
-        static_cast<__nv_bfloat16*>(dz), ld_d, status);
-  else
-    distill_backward_kernel<<<B, DTHREADS, 0, stream>>>(static_cast<const float*>(z), ld, V, idx,
-                                                        teacher, k, T, lse, dloss,
-                                                        static_cast<float*>(dz), ld_d, status);
-  return cudaGetLastError();
+  DistillArgs a = args_of(z, ld, B, V, idx, teacher, k, T, status);
+  a.lse = const_cast<float*>(lse), a.dloss = dloss, a.dz = dz, a.ld_d = ld_d;
+  return dispatch_type<kBwd>(a, dtype, stream);
+}
+
+cudaError_t launch_distill_train(const void* z, int dtype, int64_t ld, int B, int V,
+                                 const int64_t* idx, const float* teacher, int k, float T,
+                                 const float* dloss, float* loss, float* lse, void* dz,
+                                 int64_t ld_d, int* status, cudaStream_t stream) {
+  // a row that a cluster's rings hold; longer ones are read twice
+  const int64_t most = (int64_t)kMaxSlices * kTrainChunks * kChunkVecs * (dtype == PKM_BF16 ? 8 : 4);
+  if (V > most) {
+    cudaError_t e =
+        launch_distill(z, dtype, ld, B, V, idx, teacher, k, T, loss, lse, status, stream);
+    return e != cudaSuccess ? e
+                            : launch_distill_backward(z, dtype, ld, B, V, idx, teacher, k, T, lse,
+                                                      dloss, dz, ld_d, status, stream);
+  }
+  DistillArgs a = args_of(z, ld, B, V, idx, teacher, k, T, status);
+  a.loss = loss, a.lse = lse, a.dloss = dloss, a.dz = dz, a.ld_d = ld_d;
+  return dispatch_type<kTrain>(a, dtype, stream);
 }
 
 }  // namespace pkm
@@ -214,7 +824,7 @@ namespace {
 __device__ int g_distill_status;  // for calls that pass none
 
 int distill_check(int dtype, int64_t ld, int B, int V, int k, float T) {
-  if (B < 0 || V < 1 || k < 1 || !(T > 0.0f) || isinf(T)) return PKM_ERR_INVALID;
+  if (B < 0 || V < 1 || k < 1 || !(T >= 1e-30f) || isinf(T)) return PKM_ERR_INVALID;
   if (dtype != PKM_F32 && dtype != PKM_BF16) return PKM_ERR_UNSUPPORTED;
   if (k > PKM_DISTILL_MAX_K) return PKM_ERR_UNSUPPORTED;
   if (ld < V) return PKM_ERR_RANGE;
@@ -286,10 +896,8 @@ extern "C" int pkm_distill_train(const void* logits, int logit_dtype, int64_t ld
   int* st;
   if ((rc = distill_status(status, &st))) return rc;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pkm::launch_distill(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature, loss, lse,
-                          st, s) != cudaSuccess ||
-      pkm::launch_distill_backward(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature,
-                                   lse, dloss, dlogits, ld_d, st, s) != cudaSuccess)
-    return PKM_ERR_CUDA;
-  return PKM_OK;
+  return pkm::launch_distill_train(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature,
+                                   dloss, loss, lse, dlogits, ld_d, st, s) == cudaSuccess
+             ? PKM_OK
+             : PKM_ERR_CUDA;
 }

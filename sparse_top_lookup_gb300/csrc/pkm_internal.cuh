@@ -177,6 +177,10 @@ cudaError_t launch_distill_backward(const void* z, int dtype, int64_t ld, int B,
                                     const int64_t* idx, const float* teacher, int k, float T,
                                     const float* lse, const float* dloss, void* dz, int64_t ld_d,
                                     int* status, cudaStream_t stream);
+cudaError_t launch_distill_train(const void* z, int dtype, int64_t ld, int B, int V,
+                                 const int64_t* idx, const float* teacher, int k, float T,
+                                 const float* dloss, float* loss, float* lse, void* dz,
+                                 int64_t ld_d, int* status, cudaStream_t stream);
 
 // Limits of each path (checked on the host before a launch).
 constexpr int kSimtMaxK = 64;

@@ -163,6 +163,39 @@ def test_more_rows_than_run_at_once(dtype):
     check(z, idx, t, dl, 1.0, calls(z, idx, t, dl, 1.0))
 
 
+# many rows of every form: a warp each, one CTA each, clusters of two to eight; a row longer than
+# a cluster holds
+@pytest.mark.parametrize("dtype,B,V,ld", [(BF16, 700, 2001, 2003), (F32, 650, 1000, 1001),
+                                          (BF16, 700, 500, 512), (F32, 610, 64, 67),
+                                          (BF16, 620, 4000, 4001), (F32, 330, 20000, 20000),
+                                          (BF16, 200, 60001, 60001), (F32, 70, 90000, 90001),
+                                          (BF16, 4, 262160, 262160), (F32, 3, 131080, 131081),
+                                          (F32, 2, 200001, 200001), (BF16, 2, 300003, 300007),
+                                          (F32, 5, 390000, 390001), (BF16, 2, 800003, 800003),
+                                          (F32, 2, 400001, 400004)])
+def test_rows_of_every_form(dtype, B, V, ld):
+    z, idx, t, dl = make(B, V, 10, dtype, 2.0, V, ld=ld)
+    check(z, idx, t, dl, 2.0, calls(z, idx, t, dl, 2.0))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", [(3, 600), (700, 600), (3, 30000)])
+def test_rows_whose_every_logit_is_the_lowest_value(dtype, B, V):
+    # the softmax of equal logits is uniform; in one call, as lse in fp32 cannot hold log V here
+    z, idx, t, _ = make(B, V, 4, dtype, 1.0, 3)
+    z.t.fill_(torch.finfo(dtype).min)
+    idx[:] = torch.arange(4, device="cuda")
+    loss, lse, dz = torch.empty(B, device="cuda"), torch.empty(B, device="cuda"), torch.empty_like(z.t)
+    pk.check(pk.pkm_distill_train(z.t, KIND[dtype], V, B, V, idx, t, 4, 1.0,
+                                  torch.ones(B, device="cuda"), loss, lse, dz, V), "train")
+    p = torch.softmax(t.double(), 1)
+    want = torch.full((B, V), 1 / V, dtype=F64, device="cuda")
+    want[:, :4] -= p
+    half = U if dtype == F32 else 2.0 ** -8
+    assert bool(((dz.double() - want).abs() <= (half + 100 * U) * want.abs() + 100 * U / V).all())
+    assert torch.isfinite(loss).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_masked_columns_and_lists(dtype):
     z, idx, t, dl = make(12, 700, 6, dtype, 1.0, 31, masked=100)
