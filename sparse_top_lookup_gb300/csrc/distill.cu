@@ -189,47 +189,57 @@ struct List {
 };
 constexpr int kListBytes = 20;  // per entry
 
-// By one warp: loads the list of row b and forms p.  Returns the largest t (-inf for an
-// empty list) and the sum of exp((t - largest) / T).
+// One warp's loader of lists.  begin() asks for a row's first 64 entries, end() (some time later)
+// for the rest and for the student's logits there, and forms p.
 template <typename E>
-__device__ Sum load_list(const List& l, const DistillArgs& a, int64_t b, float c, int lane,
-                         bool report) {
-  const E* row = static_cast<const E*>(a.z) + b * a.ld;
-  float tm = -INFINITY;
-  for (int j = lane; j < a.kpad; j += 32) {
-    int at = -1;
-    float t = -INFINITY, zj = 0.0f;
-    if (j < a.k) {
-      const int64_t i = a.idx[b * a.k + j];
-      t = a.teacher[b * a.k + j];
-      if (i >= a.V && report) atomicExch(a.status, PKM_ERR_BAD_INDEX);
-      if (i >= 0 && i < a.V && t != -INFINITY) {
-        at = (int)i;
-        zj = El<E>::get(row[i]);
-        tm = t > tm || isnan(t) ? t : tm;
-      }
+struct ListLoader {
+  int64_t i[2];
+  float t[2];
+  __device__ void begin(const DistillArgs& a, int64_t b, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = h * 32 + lane;
+      i[h] = -1, t[h] = -INFINITY;
+      if (j < a.k) i[h] = a.idx[b * a.k + j], t[h] = a.teacher[b * a.k + j];
     }
-    l.idx[j] = at, l.t[j] = t, l.z[j] = zj;
   }
+  // Returns the largest t (-inf for an empty list) and the sum of exp((t - largest) / T).
+  __device__ Sum end(const List& l, const DistillArgs& a, int64_t b, float c, int lane,
+                     bool report) {
+    const E* row = static_cast<const E*>(a.z) + b * a.ld;
+    float tm = -INFINITY;
+    auto entry = [&](int j, int64_t ij, float tj) {
+      if (j >= a.kpad) return;
+      if (ij >= a.V && report) atomicExch(a.status, PKM_ERR_BAD_INDEX);
+      const bool there = ij >= 0 && ij < a.V && tj != -INFINITY;
+      l.idx[j] = there ? (int)ij : -1;
+      l.t[j] = tj;
+      l.z[j] = there ? El<E>::get(row[ij]) : 0.0f;
+      if (there) tm = tj > tm || isnan(tj) ? tj : tm;
+    };
+    entry(lane, i[0], t[0]);
+    entry(32 + lane, i[1], t[1]);
+    for (int j = 64 + lane; j < a.kpad; j += 32)
+      entry(j, j < a.k ? a.idx[b * a.k + j] : -1, j < a.k ? a.teacher[b * a.k + j] : -INFINITY);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float v = __shfl_xor_sync(0xffffffffu, tm, o);
-    tm = v > tm || isnan(v) ? v : tm;
-  }
-  float total = 0.0f;
-  for (int j = lane; j < a.kpad; j += 32) {
-    const float e = l.idx[j] >= 0 ? ex2((l.t[j] - tm) * c) : 0.0f;
-    l.p[j] = e;
-    total += e;
-  }
+    for (int o = 16; o; o >>= 1) {
+      const float v = __shfl_xor_sync(0xffffffffu, tm, o);
+      tm = v > tm || isnan(v) ? v : tm;
+    }
+    float total = 0.0f;
+    for (int j = lane; j < a.kpad; j += 32) {
+      const float e = l.idx[j] >= 0 ? ex2((l.t[j] - tm) * c) : 0.0f;
+      l.p[j] = e;
+      total += e;
+    }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const float inv = total > 0.0f || isnan(total) ? 1.0f / total : 0.0f;
-  for (int j = lane; j < a.kpad; j += 32) l.p[j] *= inv;
-  return Sum{tm, total};
-}
-
-// By one warp: loss and lse of row b from its sum and its list (ls: what load_list returned).
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = total > 0.0f || isnan(total) ? 1.0f / total : 0.0f;
+    for (int j = lane; j < a.kpad; j += 32) l.p[j] *= inv;
+    return Sum{tm, total};
+  }
+};
+// By one warp: loss and lse of row b from its sum and its list (ls: what loading it returned).
 // The loss is a small difference of its terms: those are in 64 bits.
 __device__ void put_loss(const DistillArgs& a, int64_t b, const Sum& sum, const List& list,
                          const Sum& ls, int lane) {
@@ -278,21 +288,27 @@ __device__ __forceinline__ Grad<true> grad_of(float lse, float g, float c) {
   return {c, lse == -INFINITY ? 0.0f : lse * 0.25f * kLog2e, lse < INFINITY ? g : NAN};
 }
 
-// By `threads` threads: the gradients of the listed columns, from z as it was (dz may be z).
+// By `threads` threads (whole warps): the gradients of the listed columns, from z as it was (dz
+// may be z).  Four threads to an entry share the search for others that name its column.
 template <typename G>
-__device__ void list_grad(const List& list, const DistillArgs& a, const G& q, float g, int tid,
-                          int threads) {
-  for (int j = tid; j < a.k; j += threads) {
-    const int at = list.idx[j];
-    if (at < 0) continue;
-    float p = 0.0f;  // of every entry that names this column
-    for (int l = 0; l < a.kpad; l += 4) {
-      const int4 i4 = *reinterpret_cast<const int4*>(list.idx + l);
-      const float4 p4 = *reinterpret_cast<const float4*>(list.p + l);
-      p += (i4.x == at ? p4.x : 0.0f) + (i4.y == at ? p4.y : 0.0f) +
-           (i4.z == at ? p4.z : 0.0f) + (i4.w == at ? p4.w : 0.0f);
-    }
-    list.dz[j] = fmaf(-g, p, q(list.z[j]));
+__device__ __forceinline__ void list_grad(const List& list, const DistillArgs& a, const G& q,
+                                          float g, int tid, int threads) {
+  const int part = tid & 3;
+  for (int j0 = 0; j0 < a.kpad; j0 += threads / 4) {
+    const int j = j0 + (tid >> 2);
+    if (j0 + ((tid & ~31) >> 2) >= a.kpad) break;  // (a whole warp)
+    const int at = j < a.kpad ? list.idx[j] : -1;
+    float p = 0.0f;
+    if (at >= 0)
+      for (int l = 4 * part; l < a.kpad; l += 16) {
+        const int4 i4 = *reinterpret_cast<const int4*>(list.idx + l);
+        const float4 p4 = *reinterpret_cast<const float4*>(list.p + l);
+        p += (i4.x == at ? p4.x : 0.0f) + (i4.y == at ? p4.y : 0.0f) +
+             (i4.z == at ? p4.z : 0.0f) + (i4.w == at ? p4.w : 0.0f);
+      }
+    p += __shfl_xor_sync(0xffffffffu, p, 1);
+    p += __shfl_xor_sync(0xffffffffu, p, 2);
+    if (at >= 0 && part == 0) list.dz[j] = fmaf(-g, p, q(list.z[j]));
   }
 }
 
@@ -373,17 +389,21 @@ __device__ __forceinline__ uint4 masked_vector() {
   return make_uint4(El<E>::kNegInf, El<E>::kNegInf, El<E>::kNegInf, El<E>::kNegInf);
 }
 
-// kFwd and kTrain for short rows: a warp each, which keeps the row in registers, kNV vectors per
-// lane, between its sum and its gradient.
+// Short rows: a warp each, which keeps the row in registers, kNV vectors per lane, between its
+// sum and its gradient.
 template <typename E, int kNV, int kMode>
-__global__ void __launch_bounds__(DTHREADS)
+__global__ void __launch_bounds__(DTHREADS, kNV == 2 ? 4 : 3)
 distill_warp_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ uint4 s_stage[kMode == kFwd ? 1 : DTHREADS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float c = kLog2e / a.T;
   const List list(smem + (size_t)warp * kListBytes * a.kpad, a.kpad);
-  for (int64_t b = (int64_t)blockIdx.x * DWARPS + warp; b < a.B; b += (int64_t)gridDim.x * DWARPS) {
+  const int64_t step = (int64_t)gridDim.x * DWARPS;
+  int64_t b = (int64_t)blockIdx.x * DWARPS + warp;
+  ListLoader<E> loader;
+  if (b < a.B) loader.begin(a, b, lane);
+  for (; b < a.B; b += step) {
     const Row<E> row(a, b, 0, 0, lane);
     uint4 d[kNV];
 #pragma unroll
@@ -391,16 +411,23 @@ distill_warp_kernel(const DistillArgs a) {
       d[j] = j * 32 + lane < row.nvec ? __ldcs(row.vec + j * 32 + lane) : masked_vector<E>();
     const float x = row.extra >= 0 ? El<E>::get(row.z[row.extra]) : -INFINITY;
     const float g = kMode == kFwd ? 0.0f : a.dloss[b] * a.T;
-    const Sum ls = load_list<E>(list, a, b, c, lane, true);
+    const float lse = kMode == kBwd ? a.lse[b] : 0.0f;
+    const Sum ls = loader.end(list, a, b, c, lane, true);
+    if (b + step < a.B) loader.begin(a, b + step, lane);
     Sum sum{-INFINITY, 0.0f};
-    add_vectors<E>(sum, d, c);
-    add_one(sum, x, c);
-    sum = lanes_join<32>(sum, c);
+    if constexpr (kMode != kBwd) {
+      add_vectors<E>(sum, d, c);
+      add_one(sum, x, c);
+      sum = lanes_join<32>(sum, c);
+    }
     __syncwarp();
-    put_loss(a, b, sum, list, ls, lane);
-    if constexpr (kMode == kTrain) {
+    if constexpr (kMode != kBwd) put_loss(a, b, sum, list, ls, lane);
+    if constexpr (kMode != kFwd) {
       const bool zero = g == 0.0f || ls.m == -INFINITY;  // no gradient, whatever z holds
-      const Grad<false> q = grad_of(sum, g, c);
+      const auto q = [&] {
+        if constexpr (kMode == kBwd) return grad_of(lse, g, c);
+        else return grad_of(sum, g, c);
+      }();
       if (!zero) list_grad(list, a, q, g, lane, 32);
       E* out = static_cast<E*>(a.dz) + b * a.ld_d;
       const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
@@ -430,6 +457,8 @@ distill_backward_kernel(const DistillArgs a) {
   const float c = kLog2e / a.T;
   const List list(smem, a.kpad);
   const int64_t units = (int64_t)a.B << a.lsh;
+  ListLoader<E> loader;
+  if (warp == 0) loader.begin(a, blockIdx.x >> a.lsh, lane);
   for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int64_t b = unit >> a.lsh;
     const int slice = (int)(unit & ((1 << a.lsh) - 1));
@@ -444,8 +473,9 @@ distill_backward_kernel(const DistillArgs a) {
     const float g = a.dloss[b] * a.T;
     const Grad<true> q = grad_of(a.lse[b], g, c);
     if (warp == 0) {
-      const Sum ls = load_list<E>(list, a, b, c, lane, slice == 0);
+      const Sum ls = loader.end(list, a, b, c, lane, slice == 0);
       if (lane == 0) s_ls = ls;
+      if (unit + gridDim.x < units) loader.begin(a, (unit + gridDim.x) >> a.lsh, lane);
     }
     __syncthreads();
     const bool zero = g == 0.0f || s_ls.m == -INFINITY;
@@ -468,32 +498,58 @@ distill_backward_kernel(const DistillArgs a) {
 }
 
 // kFwd and kTrain: a CTA per slice of a row, a cluster per row.
-//   warps 0..7  (data) each chunk of the slice: maximum and sum; the slice's sums are exchanged
-//               between the cluster's CTAs through shared memory (st.async); then (kTrain)
-//               each chunk again: the gradient, written out;
-//   warp 8      (list) the loss, and the next row's list;
-//   warp 9      (copies) the slices' chunks by bulk copies into a ring of slots.
-// In kTrain a slot is free when its gradient is written, and the ring holds two rows' slices: a
-// row is loaded while the one before it is worked on.
-constexpr int kStreamThreads = DTHREADS + 64;
+//   data warps  each chunk of the slice: maximum and sum (first pass); the slice's sums go to the
+//               cluster's other CTAs through shared memory (st.async); then (kTrain) each chunk
+//               again: the gradient, written out (second pass);
+//   list warp   the rows' lists; the loss, by the slices in turn;
+//   copy warp   the slices' chunks by bulk copies into a ring of slots.
+// A row's second pass comes after the next row's first, so the exchange costs no waiting, and
+// in kTrain a slot is free when its gradient is written: the ring holds up to three rows'
+// slices, one in each pass and one on its way.
+//
+// Order.  Per row i there is one barrier of data and list warps, B(i), after its first pass and
+// its list.  Then a data thread sends the slice's sum, and:
+//   data warps  B(i), send i, second pass of i - 1, first pass of i + 1, B(i + 1), ...
+//   list warp   B(i), loss of i - 1, list of i + 1, B(i + 1), ...
+// - list i is in use until the second pass of i ends, before B(i + 2): three copies of a list;
+// - dz may be z: row i is written after every CTA of the cluster has sent its sum, so after
+//   every list warp has read row i;
+// - warps' sums i are read until B(i + 2), by the list warp: three copies;
+// - slices' sums i are read before B(i + 2), and another CTA sends its sum i + 4 after it has
+//   waited for this CTA's sum i + 2 (in its second pass of i + 2; in kFwd for that alone), sent
+//   after B(i + 2): four copies.
+constexpr int kCopies = 4;
 constexpr int kMaxSlots = 16;
-constexpr size_t kDynamic = 220 * 1024;  // dynamic shared memory at most
-constexpr int kTrainChunks = 12;  // of a slice, at most: they fit beside the longest lists
-constexpr int kChunkVecs = 4 * DTHREADS;  // 16 KB: 4 vectors per thread
-
-static_assert(kTrainChunks * 16 * kChunkVecs + 2 * kListBytes * PKM_DISTILL_MAX_K <= kDynamic,
+constexpr int kChunkVecs = 2048;        // 32 KB
+constexpr size_t kDynamic = 216 * 1024;  // dynamic shared memory at most
+constexpr int kTrainChunks = 2;  // of a slice, at most: two slices fit beside the longest lists
+static_assert(2 * kTrainChunks * 16 * kChunkVecs + 3 * kListBytes * PKM_DISTILL_MAX_K <= kDynamic,
               "ring of the longest slices");
 
+// What the data warps need of a row, written by the copy warp before the row's first chunk.
+template <typename E>
+struct Geo {
+  E* body;   // dz at the slice's first vector
+  const E* z;
+  float g;   // dloss * T
+  int n;     // vectors of the slice
+  int head, nvec, v0, ends;  // as in Row; ends: elements outside the vectors (slice 0: else 0)
+  int same;  // z's and dz's rows start alike within 16 bytes
+};
+
+constexpr int kData = DWARPS;
 template <typename E, int kMode>
-__global__ void __launch_bounds__(kStreamThreads, 3)
+__global__ void __launch_bounds__(kData * 32 + 64, kMode == kTrain ? 2 : 3)
 distill_stream_kernel(const DistillArgs a) {
   using namespace tc;
+  constexpr int kThreads = kData * 32, kPer = El<E>::kPerVec;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint4 s_stage[kMode == kFwd ? 1 : DTHREADS];
-  __shared__ Sum s_warp[2][DWARPS];
-  __shared__ __align__(8) Sum s_slice[2][kMaxSlices];
-  __shared__ Sum s_ls[2];
-  __shared__ __align__(8) uint64_t s_bars[2 * kMaxSlots + 2];
+  __shared__ uint4 s_stage[kMode == kFwd ? 1 : kThreads];
+  __shared__ Sum s_warp[3][kData];
+  __shared__ __align__(8) Sum s_slice[kCopies][kMaxSlices];
+  __shared__ Sum s_ls[3];
+  __shared__ __align__(16) Geo<E> s_geo[kCopies];
+  __shared__ __align__(8) uint64_t s_bars[2 * kMaxSlots + kCopies];
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = kLog2e / a.T;
@@ -505,14 +561,13 @@ distill_stream_kernel(const DistillArgs a) {
   const uint32_t bar0 = smem_u32(s_bars);
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
   auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxSlots + s); };
-  auto bar_sums = [&](int par) { return bar0 + 8u * (2 * kMaxSlots + par); };
+  auto bar_sums = [&](int i) { return bar0 + 8u * (2 * kMaxSlots + i); };
   if (tid == 0) {
     for (int s = 0; s < slots; ++s) {
       mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), DWARPS);
+      mbar_init(bar_empty(s), kData);
     }
-    mbar_init(bar_sums(0), 1);
-    mbar_init(bar_sums(1), 1);
+    for (int i = 0; i < kCopies; ++i) mbar_init(bar_sums(i), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -520,25 +575,46 @@ distill_stream_kernel(const DistillArgs a) {
   if (slices > 1) cluster_sync();  // every CTA's barriers exist before its memory is written
   const Ctl ctl{&s_abort, a.status};
 
-  const int64_t units = (int64_t)a.B << lsh;
+  // this CTA's slice (consecutive CTAs, a cluster's, have those of one row) of rows first + i *
+  // every, i < count
   const int slice = (int)(blockIdx.x & (slices - 1));
-  // consecutive CTAs (a cluster's) take the slices of one row
-  if (warp == DWARPS + 1) {
+  const int64_t first = blockIdx.x >> lsh, every = gridDim.x >> lsh;
+  const int count = (int)((a.B - first + every - 1) / every);
+  auto row_at = [&](int i) { return first + i * every; };
+  if (warp == kData + 1) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
       int s = 0, issued = 0;
       uint32_t ph = 1;
       bool ok = true;
-      for (int64_t unit = blockIdx.x; ok && unit < units; unit += gridDim.x) {
-        const Row<E> row(a, unit >> lsh, slice, lsh, 0);
-        for (int v = row.v0; v < row.v1; v += chunk) {
+      for (int i = 0; ok && i < count; ++i) {
+        const int64_t b = row_at(i);
+        const Row<E> row(a, b, slice, lsh, 0);
+        Geo<E> geo;
+        E* out = static_cast<E*>(a.dz) + b * a.ld_d + row.head;
+        geo.body = out + (int64_t)row.v0 * kPer;
+        geo.z = row.z;
+        geo.g = kMode == kTrain ? a.dloss[b] * a.T : 0.0f;
+        geo.n = row.v1 - row.v0;
+        geo.head = row.head, geo.nvec = row.nvec, geo.v0 = row.v0;
+        geo.ends = slice == 0 ? a.V - row.nvec * kPer : 0;
+        geo.same = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+        int v = 0;
+        do {  // (a slice without vectors is one empty chunk)
           if (!(ok = wait_phase(bar_empty(s), ph, ctl))) break;
-          const uint32_t bytes = 16u * min(chunk, row.v1 - v);
-          mbar_expect_tx(bar_full(s), bytes);
-          bulk_load(smem_u32(ring + (size_t)s * chunk), row.vec + v, bytes, bar_full(s));
+          // the slot is free, so its row's predecessors up to kCopies back are done with
+          if (v == 0) s_geo[i % kCopies] = geo;
+          const uint32_t bytes = 16u * min(chunk, geo.n - v);
+          if (bytes) {
+            mbar_expect_tx(bar_full(s), bytes);
+            bulk_load(smem_u32(ring + (size_t)s * chunk), row.vec + row.v0 + v, bytes, bar_full(s));
+          } else {
+            mbar_arrive(bar_full(s));
+          }
           if (issued < slots) ++issued;
           if (++s == slots) s = 0, ph ^= 1u;
-        }
+          v += chunk;
+        } while (v < geo.n);
       }
       // (normally the data warps have waited for them all) no copy outlives the CTA
       for (int i = 0; i < issued; ++i) {
@@ -548,110 +624,134 @@ distill_stream_kernel(const DistillArgs a) {
     }
     return;
   }
-  // The list warp meets the data warps once a row, where the list is needed: it has the time of
-  // a row for the loss and the next row's list.  What it still reads then is kept twice (par).
-  const bool data = warp < DWARPS;
-  auto fetch = [&](int64_t unit, int par) {
-    if (unit >= units) return;
-    const Sum ls = load_list<E>(list_at(par), a, unit >> lsh, c, lane, slice == 0);
-    if (lane == 0) s_ls[par] = ls;
+  auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads + 32) : "memory"); };
+  // the row's sum, once every slice's has come
+  auto sum_of = [&](int i) {
+    if (slices == 1) return lanes_join<kData>(s_warp[i % 3][lane & (kData - 1)], c);
+    wait_phase_cluster(bar_sums(i % kCopies), (uint32_t)(i / kCopies) & 1u, ctl);
+    __syncwarp();
+    return lanes_join<kMaxSlices>(lane % kMaxSlices < slices
+                                      ? s_slice[i % kCopies][lane % kMaxSlices]
+                                      : Sum{-INFINITY, 0.0f}, c);
   };
-  if (!data) fetch(blockIdx.x, 0);
-  int s1 = 0, s2 = 0;         // next slot of the first and the second pass
-  uint32_t ph = 0, sums = 0;  // its parity in the first; bit par: that of bar_sums(par)
-  float x_next = -INFINITY, g_next = 0.0f;
-  auto ahead = [&](int64_t unit) {  // what the row takes from memory besides the chunks
-    if (!data || unit >= units) return;
-    const Row<E> row(a, unit >> lsh, slice, lsh, tid);
-    x_next = row.extra >= 0 ? El<E>::get(row.z[row.extra]) : -INFINITY;
-    if (kMode == kTrain) g_next = a.dloss[unit >> lsh] * a.T;
-  };
-  ahead(blockIdx.x);
-  int par = 0;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, par ^= 1) {
-    const int64_t b = unit >> lsh;
-    const Row<E> row(a, b, slice, lsh, tid);
-    const List list = list_at(par);
-    const float x = x_next, g = g_next;
-    Sum sum{-INFINITY, 0.0f};
-    if (data) {
-      for (int v = row.v0; v < row.v1; v += chunk) {
-        wait_phase(bar_full(s1), ph, ctl);
-        const uint4* src = ring + (size_t)s1 * chunk;
-        const int n = min(chunk, row.v1 - v);
-        uint4 d[kChunkVecs / DTHREADS];
+  if (warp == kData) {
+    // ---------------------------------------------------------------- lists and losses
+    // (kFwd needs a row's list for its loss alone)
+    auto wanted = [&](int i) {
+      return i < count && (kMode == kTrain || (i & (slices - 1)) == slice);
+    };
+    ListLoader<E> loader;
+    auto list = [&](int i) {
+      if (!wanted(i)) return;
+      const Sum ls = loader.end(list_at(i % 3), a, row_at(i), c, lane, (i & (slices - 1)) == slice);
+      if (lane == 0) s_ls[i % 3] = ls;
+      __syncwarp();
+    };
+    if (wanted(0)) loader.begin(a, row_at(0), lane);
+    list(0);
+    if (wanted(1)) loader.begin(a, row_at(1), lane);
+    for (int i = 0; i <= count; ++i) {
+      if (i < count) meet();  // B(i)
+      if (i > 0 && ((i - 1) & (slices - 1)) == slice)
+        put_loss(a, row_at(i - 1), sum_of(i - 1), list_at((i - 1) % 3), s_ls[(i - 1) % 3], lane);
+      list(i + 1);
+      if (wanted(i + 2)) loader.begin(a, row_at(i + 2), lane);
+    }
+    return;
+  }
+  // ------------------------------------------------------------------ data
+  int s1 = 0, s2 = 0;  // next slot of the first and the second pass
+  uint32_t ph = 0;     // its parity in the first
+  float x = -INFINITY, x_last;  // this thread's element outside the vectors
+  for (int i = 0; i <= count; ++i) {
+    x_last = x;
+    if (i < count) {
+      Sum sum{-INFINITY, 0.0f};
+      wait_phase(bar_full(s1), ph, ctl);
+      const Geo<E>& geo = s_geo[i % kCopies];
+      const int total = geo.n;
+      x = -INFINITY;
+      if (tid < geo.ends) x = El<E>::get(geo.z[tid < geo.head ? tid : geo.nvec * kPer + tid]);
+      for (int v = 0;;) {
+        const uint4* src = ring + (size_t)s1 * chunk + tid;
+        const int n = min(chunk, total - v);
+        constexpr int kNV = kChunkVecs / kThreads;
+        uint4 d[kNV];
 #pragma unroll
-        for (int j = 0; j < kChunkVecs / DTHREADS; ++j)
-          d[j] = j * DTHREADS + tid < n ? src[j * DTHREADS + tid] : masked_vector<E>();
+        for (int j = 0; j < kNV; ++j)
+          d[j] = j * kThreads + tid < n ? src[j * kThreads] : masked_vector<E>();
         if constexpr (kMode == kFwd) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_empty(s1));
         }
         add_vectors<E>(sum, d, c);
         if (++s1 == slots) s1 = 0, ph ^= 1u;
+        if ((v += chunk) >= total) break;
+        wait_phase(bar_full(s1), ph, ctl);
       }
-      add_one(sum, x, c);
-      ahead(unit + gridDim.x);
+      if (geo.ends) add_one(sum, x, c);
       sum = lanes_join<32>(sum, c);
-      if (lane == 0) s_warp[par][warp] = sum;
+      if (lane == 0) s_warp[i % 3][warp] = sum;
+      meet();  // B(i)
+      if (slices > 1 && warp == 0) {
+        if (kMode == kFwd && i > 1) sum_of(i - 2);
+        sum = lanes_join<kData>(s_warp[i % 3][lane & (kData - 1)], c);
+        const uint32_t bar = bar_sums(i % kCopies);
+        if (lane == 0) mbar_expect_tx(bar, 8u * slices);
+        if (lane < slices)
+          asm volatile(
+              "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, "
+              "[%3];" ::"r"(mapa_shared(smem_u32(&s_slice[i % kCopies][slice]), lane)),
+              "r"(__float_as_uint(sum.m)), "r"(__float_as_uint(sum.s)),
+              "r"(mapa_shared(bar, lane))
+              : "memory");
+      }
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(DTHREADS + 32) : "memory");
-    sum = lanes_join<DWARPS>(s_warp[par][lane & (DWARPS - 1)], c);
-    if (slices > 1) {
-      // each CTA's sum to every CTA of the cluster, completing on the receiver's barrier.
-      // Two copies of s_slice: a CTA sends a row's sum after it has those of the row before,
-      // so after every other has read those of the row before that.
-      const uint32_t bar = bar_sums(par);
-      if (tid == 0) mbar_expect_tx(bar, 8u * slices);
-      if (tid < slices)
-        asm volatile(
-            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
-                "r"(mapa_shared(smem_u32(&s_slice[par][slice]), tid)),
-            "r"(__float_as_uint(sum.m)), "r"(__float_as_uint(sum.s)), "r"(mapa_shared(bar, tid))
-            : "memory");
-      wait_phase_cluster(bar, (sums >> par) & 1u, ctl);
-      sums ^= 1u << par;
-      __syncwarp();
-      sum = lanes_join<kMaxSlices>(lane % kMaxSlices < slices ? s_slice[par][lane % kMaxSlices]
-                                                              : Sum{-INFINITY, 0.0f}, c);
-    }
-    const Sum ls = s_ls[par];
-    if (!data) {
-      if (slice == 0) put_loss(a, b, sum, list, ls, lane);
-      fetch(unit + gridDim.x, par ^ 1);
-      continue;
-    }
-    if constexpr (kMode == kTrain) {
-      const bool zero = g == 0.0f || ls.m == -INFINITY;  // no gradient, whatever z holds
-      const Grad<false> q = grad_of(sum, g, c);
-      if (!zero) list_grad(list, a, q, g, tid, DTHREADS);
-      E* out = static_cast<E*>(a.dz) + b * a.ld_d;
-      const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
-      for (int v = row.v0; v < row.v1; v += chunk) {
+    if (kMode == kTrain && i > 0) {
+      const Geo<E>& geo = s_geo[(i - 1) % kCopies];
+      const List list = list_at((i - 1) % 3);
+      const float g = geo.g;
+      const bool zero = g == 0.0f || s_ls[(i - 1) % 3].m == -INFINITY;  // whatever z holds
+      const Grad<false> q = grad_of(sum_of(i - 1), g, c);
+      if (!zero) list_grad(list, a, q, g, tid, kThreads);
+      E* body = geo.body;
+      const int total = geo.n;
+      const bool same = geo.same;
+      for (int v = 0; v < total || v == 0; v += chunk) {
         const uint4* src = ring + (size_t)s2 * chunk;
-        const int n = min(chunk, row.v1 - v);
+        const int n = min(chunk, total - v);
 #pragma unroll
-        for (int j = 0; j < kChunkVecs / DTHREADS; ++j) {
-          const int i = j * DTHREADS + tid;
-          if (i - lane >= n) break;
-          put_vector(out + row.head, v + i, v + n, i < n ? src[i] : masked_vector<E>(), q, zero,
+        for (int j = 0; j < kChunkVecs / kThreads; ++j) {
+          const int at = j * kThreads + tid;
+          if (at - lane >= n) break;
+          put_vector(body + (int64_t)v * kPer, at, n, at < n ? src[at] : masked_vector<E>(), q, zero,
                      same, s_stage + warp * 32, lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty(s2));
         if (++s2 == slots) s2 = 0;
       }
-      if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
+      if (tid < geo.ends) {
+        E* out = body - ((int64_t)geo.v0 * kPer + geo.head);
+        El<E>::put(out + (tid < geo.head ? tid : geo.nvec * kPer + tid), zero ? 0.0f : q(x_last));
+      }
       // the listed columns' values replace those of the row
-      asm volatile("bar.sync 2, %0;" ::"n"(DTHREADS) : "memory");
-      if (!zero)
-        for (int j = tid; j < a.k; j += DTHREADS) {
+      asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+      if (!zero) {
+        E* out = body - ((int64_t)geo.v0 * kPer + geo.head);
+        for (int j = tid; j < a.k; j += kThreads) {
           const int at = list.idx[j];
-          if (at >= 0 && row.mine(at, slice)) El<E>::put(out + at, list.dz[j]);
+          if (at < 0) continue;
+          const bool outside = at < geo.head || at >= geo.head + geo.nvec * kPer;
+          const int v = (at - geo.head) / kPer - geo.v0;
+          if (outside ? slice == 0 : v >= 0 && v < total) El<E>::put(out + at, list.dz[j]);
         }
+      }
     }
   }
-  // (a CTA leaves after its last row's wait: no other writes into its shared memory after that)
+  // (the other CTAs' last sums may still be on their way here)
+  if (kMode == kFwd && slices > 1 && warp == 0)
+    for (int i = max(0, count - 2); i < count; ++i) sum_of(i);
 }
 
 // CTAs that run at one time at most, for a grid that leaves no second round to a few.
@@ -693,33 +793,17 @@ cudaError_t launch_backward(DistillArgs& a, cudaStream_t stream) {
 }
 
 template <typename E, int kMode>
-cudaError_t launch_stream(DistillArgs& a, cudaStream_t stream) {
-  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
-  // slices of at most 32 KB; more and smaller ones while CTAs are few
-  while (a.lsh < kMaxLsh && nvec > (int64_t)2 * kChunkVecs << a.lsh) ++a.lsh;
-  while (a.lsh < kMaxLsh && ((int64_t)a.B << a.lsh) * 2 <= tc::sm_count() &&
-         nvec > 2 * DTHREADS << a.lsh)
-    ++a.lsh;
-  const int slices = 1 << a.lsh;
-  const int64_t per = (nvec + slices - 1) >> a.lsh;
-  // chunks of 1 KB steps up to 16 KB, and two slices of them in the ring (kFwd: four chunks)
-  a.chunk = per >= kChunkVecs ? kChunkVecs : (int)((per + 63) / 64 * 64);
-  if (a.chunk < 64) a.chunk = 64;
-  const int64_t chunks = (per + a.chunk - 1) / a.chunk;
-  const size_t lists = (size_t)2 * kListBytes * a.kpad;
-  const int64_t room = (kDynamic - lists) / ((size_t)a.chunk * 16);
-  a.slots = kMode == kFwd ? 4 : (int)(chunks * 2 < room ? chunks * 2 : room);
-  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
-  if (a.slots < 1) a.slots = 1;  // (a row without vectors)
+cudaError_t launch_stream(const DistillArgs& a, cudaStream_t stream) {
   auto kernel = distill_stream_kernel<E, kMode>;
-  const size_t smem = (size_t)a.slots * a.chunk * 16 + lists;
+  const int slices = 1 << a.lsh;
+  const size_t smem = (size_t)a.slots * a.chunk * 16 + (size_t)3 * kListBytes * a.kpad;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = slices;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3(kData * 32 + 64);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -751,19 +835,39 @@ cudaError_t launch_stream(DistillArgs& a, cudaStream_t stream) {
 }
 
 template <typename E, int kMode>
+cudaError_t dispatch_stream(DistillArgs& a, cudaStream_t stream) {
+  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+  // slices of at most 32 KB; more and smaller ones while CTAs are few
+  while (a.lsh < kMaxLsh && nvec > (int64_t)kChunkVecs << a.lsh) ++a.lsh;
+  while (a.lsh < kMaxLsh && ((int64_t)a.B << a.lsh) * 2 <= tc::sm_count() &&
+         nvec > 2 * DTHREADS << a.lsh)
+    ++a.lsh;
+  const int64_t per = (nvec + (1 << a.lsh) - 1) >> a.lsh;
+  // chunks of up to 32 KB in steps of 1 KB, and three slices of them in the ring (kFwd: two
+  // chunks)
+  a.chunk = per >= kChunkVecs ? kChunkVecs : (int)((per + 63) / 64 * 64);
+  if (a.chunk < 64) a.chunk = 64;
+  const int64_t chunks = per ? (per + a.chunk - 1) / a.chunk : 1;
+  const int64_t room =
+      (kDynamic - (size_t)3 * kListBytes * a.kpad) / ((size_t)a.chunk * 16);
+  a.slots = kMode == kFwd ? 2 : (int)(chunks * 3 < room ? chunks * 3 : room);
+  if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+  return launch_stream<E, kMode>(a, stream);
+}
+
+template <typename E, int kMode>
 cudaError_t dispatch(DistillArgs& a, cudaStream_t stream) {
   a.kpad = (a.k + 3) / 4 * 4;
   a.lsh = 0;
-  if constexpr (kMode == kBwd) {
+  // rows of up to 4 KB, when there are enough of them to fill the GPU: a warp each
+  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+  if (nvec <= 32 * 8 && a.k <= kWarpMaxK && a.B >= 4 * tc::sm_count())
+    return nvec <= 32 * 2 ? launch_warps<E, 2, kMode>(a, stream)
+                          : launch_warps<E, 8, kMode>(a, stream);
+  if constexpr (kMode == kBwd)
     return launch_backward<E>(a, stream);
-  } else {
-    // rows of up to 4 KB, when there are enough of them to fill the GPU: a warp each
-    const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
-    if (nvec <= 32 * 8 && a.k <= kWarpMaxK && a.B >= 4 * tc::sm_count())
-      return nvec <= 32 * 2 ? launch_warps<E, 2, kMode>(a, stream)
-                            : launch_warps<E, 8, kMode>(a, stream);
-    return launch_stream<E, kMode>(a, stream);
-  }
+  else
+    return dispatch_stream<E, kMode>(a, stream);
 }
 
 template <int kMode>
