@@ -50,9 +50,14 @@ struct El<float> {
   __device__ static float get(const uint4& d, int i) {
     return __uint_as_float(i == 0 ? d.x : i == 1 ? d.y : i == 2 ? d.z : d.w);
   }
-  __device__ static float vmax(const uint4& d) {
-    return fmaxf(fmaxf(get(d, 0), get(d, 1)), fmaxf(get(d, 2), get(d, 3)));
-  }
+  // the largest value of several vectors (NaNs are passed over)
+  struct Max {
+    float m = -INFINITY;
+    __device__ void add(const uint4& d) {
+      m = fmaxf(m, fmaxf(fmaxf(get(d, 0), get(d, 1)), fmaxf(get(d, 2), get(d, 3))));
+    }
+    __device__ float value() const { return m; }
+  };
 };
 template <>
 struct El<__nv_bfloat16> {
@@ -64,11 +69,18 @@ struct El<__nv_bfloat16> {
     const uint32_t w = i < 2 ? d.x : i < 4 ? d.y : i < 6 ? d.z : d.w;
     return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
   }
-  __device__ static float vmax(const uint4& d) {
-    auto h = [](const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-    const __nv_bfloat162 m = __hmax2(__hmax2(h(d.x), h(d.y)), __hmax2(h(d.z), h(d.w)));
-    return fmaxf(__low2float(m), __high2float(m));
-  }
+  struct Max {
+    uint32_t w = kNegInf;
+    __device__ void add(const uint4& d) {
+      auto h = [](const uint32_t& v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+      const __nv_bfloat162 m =
+          __hmax2(__hmax2(h(w), __hmax2(h(d.x), h(d.y))), __hmax2(h(d.z), h(d.w)));
+      w = *reinterpret_cast<const uint32_t*>(&m);
+    }
+    __device__ float value() const {
+      return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+  };
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -80,28 +92,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&w);
-}
-
-// Two fp32 values in one register pair, and the packed arithmetic on them.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 
 // log of a positive s as a double good to about 1e-8: the exponent's part
@@ -186,6 +176,22 @@ struct List {
         z(reinterpret_cast<float*>(base) + 2 * kpad),
         p(reinterpret_cast<float*>(base) + 3 * kpad),
         dz(reinterpret_cast<float*>(base) + 4 * kpad) {}
+  // By one warp: whether a column may occur twice (lists of up to 64 are looked through).
+  __device__ bool twice(int kpad, int lane) const {
+    if (kpad > 64) return true;
+    const int i0 = lane < kpad ? idx[lane] : -1, i1 = 32 + lane < kpad ? idx[32 + lane] : -1;
+    const uint32_t self = 1u << lane;
+    bool found = __match_any_sync(0xffffffffu, i0) != self && i0 >= 0;
+    if (kpad > 32) {
+      found |= (__match_any_sync(0xffffffffu, i1) != self && i1 >= 0);
+#pragma unroll 8
+      for (int l = 0; l < 32; ++l) {
+        const int other = __shfl_sync(0xffffffffu, i1, l);
+        found |= other == i0 && i0 >= 0;
+      }
+    }
+    return __any_sync(0xffffffffu, found);
+  }
 };
 constexpr int kListBytes = 20;  // per entry
 
@@ -264,29 +270,50 @@ __device__ void put_loss(const DistillArgs& a, int64_t b, const Sum& sum, const 
   }
 }
 
-// g q(z) of a row.  In the training form from the row's sum; every q is 0 when every logit is
-// -inf.  In the backward form from an lse in fp32: a quarter of the exponent at a time (no
-// overflow), and never above 0.
-template <bool kFromLse>
+// g q(z) of a row, from its sum; every q is 0 when every logit is -inf.  With the factor
+// 2^(z c + off) ahead of `scale` the difference z - ref costs no instruction; rows whose
+// reference is so far out that ref c overflows (all logits at a mask's value) are `far` and take
+// the difference first.  For bf16 the factor |scale| goes into the exponent too (off_all; 2^-19
+// at most for it, where dz is rounded to 2^-8), and its sign into the packed result.  What the
+// rounding of off leaves is in scale_fast.
 struct Grad {
-  float c, ref, scale;
-  __device__ float operator()(float z) const {
-    if constexpr (kFromLse) return ex2(fminf(4.0f * fmaf(z, 0.25f * c, -ref), 0.0f)) * scale;
-    return ex2((z - ref) * c) * scale;
+  float c, ref, scale, scale_fast, off, off_all;
+  bool far;
+  __device__ Grad(float c, float ref, float scale) : c(c), ref(ref), scale(scale) {
+    off = -ref * c;
+    far = !(fabsf(off) < 1e37f);
+    scale_fast = scale * ex2(fmaf(-ref, c, -off));
+    off_all = off + log2f(fabsf(scale_fast));
   }
-  __device__ float2 two(float z0, float z1) const {
-    if constexpr (kFromLse) return make_float2((*this)(z0), (*this)(z1));
-    const float2 e = unpair(mul2(add2(pair(z0, z1), pair(-ref, -ref)), pair(c, c)));
-    return unpair(mul2(pair(ex2(e.x), ex2(e.y)), pair(scale, scale)));
-  }
+  __device__ float operator()(float z) const { return ex2((z - ref) * c) * scale; }
+  __device__ float fast(float z) const { return ex2(fmaf(z, c, off)) * scale_fast; }
 };
-__device__ __forceinline__ Grad<false> grad_of(const Sum& sum, float g, float c) {
-  return {c, sum.m == -INFINITY ? 0.0f : sum.m, sum.s == 0.0f ? 0.0f : __fdividef(g, sum.s)};
+__device__ __forceinline__ Grad grad_of(const Sum& sum, float g, float c) {
+  const float ref = sum.m == -INFINITY ? 0.0f : sum.m;
+  return Grad(c, ref, sum.s == 0.0f ? 0.0f : __fdividef(g, sum.s));
 }
-__device__ __forceinline__ Grad<true> grad_of(float lse, float g, float c) {
-  // (a row whose lse is NaN or +inf has no gradient)
-  return {c, lse == -INFINITY ? 0.0f : lse * 0.25f * kLog2e, lse < INFINITY ? g : NAN};
-}
+// From an lse in fp32: q = exp(z / T - lse).  In the far rows lse holds no more than the row's
+// maximum; q stays within [0, 1] there.
+struct GradLse {
+  float c, scale, off, off_all;
+  bool far;
+  __device__ GradLse(float lse, float g, float c) : c(c) {
+    // (a row whose lse is NaN or +inf has no gradient)
+    scale = lse < INFINITY ? g : NAN;
+    off = -lse * kLog2e;
+    far = !(fabsf(off) < 1e37f);
+    if (far)
+      off = -lse * (0.25f * kLog2e);
+    else
+      scale *= ex2(fmaf(-lse, kLog2e, -off));
+    if (lse == -INFINITY) scale = g, off = 0.0f, far = false;
+    off_all = off + log2f(fabsf(scale));
+  }
+  __device__ float operator()(float z) const {
+    return (far ? ex2(fminf(4.0f * fmaf(z, 0.25f * c, off), 0.0f)) : ex2(fmaf(z, c, off))) * scale;
+  }
+  __device__ float fast(float z) const { return ex2(fmaf(z, c, off)) * scale; }
+};
 
 // By `threads` threads (whole warps): the gradients of the listed columns, from z as it was (dz
 // may be z).  Four threads to an entry share the search for others that name its column.
@@ -315,19 +342,30 @@ __device__ __forceinline__ void list_grad(const List& list, const DistillArgs& a
 // One vector of dz per lane: vector v (< end) of the row's out + head, from z's vector d.  `same`:
 // the rows of z and dz start alike within 16 bytes.  Otherwise the warp's 32 vectors go
 // through `stage` and out as whole words (bf16: with single elements at the ends).
-template <typename E, typename G>
+enum Form { kZero, kFast, kSlow };
+template <Form kForm>
+struct FormOf {
+  static constexpr Form value = kForm;
+};
+template <typename E, Form kForm, typename G>
 __device__ __forceinline__ void put_vector(E* body, int v, int end, const uint4& d, const G& q,
-                                           bool zero, bool same, uint4* stage, int lane) {
+                                           bool same, uint4* stage, int lane) {
   constexpr int kPer = El<E>::kPerVec;
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < kPer; i += 2) {
-    const float2 f = q.two(El<E>::get(d, i), El<E>::get(d, i + 1));
-    if constexpr (kPer == 8) {
-      w[i / 2] = zero ? 0u : pack2(f.x, f.y);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kForm == kZero) {
+      w[i] = 0;
+    } else if constexpr (kPer == 4) {
+      const float z = El<E>::get(d, i);
+      w[i] = __float_as_uint(kForm == kFast ? q.fast(z) : q(z));
     } else {
-      w[i] = zero ? 0u : __float_as_uint(f.x);
-      w[i + 1] = zero ? 0u : __float_as_uint(f.y);
+      const float z0 = El<E>::get(d, 2 * i), z1 = El<E>::get(d, 2 * i + 1);
+      if constexpr (kForm == kFast)
+        w[i] = pack2(ex2(fmaf(z0, q.c, q.off_all)), ex2(fmaf(z1, q.c, q.off_all))) ^
+               (q.scale < 0.0f ? 0x80008000u : 0u);
+      else
+        w[i] = pack2(q(z0), q(z1));
     }
   }
   if (same) {
@@ -356,27 +394,49 @@ __device__ __forceinline__ void put_vector(E* body, int v, int end, const uint4&
   __syncwarp();
 }
 
-// sum joined with exp of vectors d, by one thread.
+// sum joined with the terms of vectors d, by one thread: 2^((z - m) c).
 template <typename E, int kNV>
 __device__ __forceinline__ void add_vectors(Sum& sum, const uint4 (&d)[kNV], float c) {
   constexpr int kPer = El<E>::kPerVec;
-  float m = sum.m;
+  typename El<E>::Max most;
 #pragma unroll
-  for (int j = 0; j < kNV; ++j) m = fmaxf(m, El<E>::vmax(d[j]));
+  for (int j = 0; j < kNV; ++j) most.add(d[j]);
+  const float m = fmaxf(sum.m, most.value());
   const float ref = m == -INFINITY ? 0.0f : m;
-  const float before = m == -INFINITY ? sum.s : sum.s * ex2((sum.m - ref) * c);
-  const uint64_t minus = pair(-ref, -ref), cc = pair(c, c);
-  uint64_t s[2] = {pair(before, 0.0f), 0};
+  float s[4] = {m == -INFINITY ? sum.s : sum.s * ex2((sum.m - ref) * c), 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < kNV; ++j)
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      const float2 e =
-          unpair(mul2(add2(pair(El<E>::get(d[j], i), El<E>::get(d[j], i + 1)), minus), cc));
-      s[(i >> 1) & 1] = add2(s[(i >> 1) & 1], pair(ex2(e.x), ex2(e.y)));
+    for (int i = 0; i < kPer; ++i) s[i & 3] += ex2((El<E>::get(d[j], i) - ref) * c);
+  sum = Sum{m, (s[0] + s[1]) + (s[2] + s[3])};
+}
+// The same for `count` vectors in shared memory, kThreads apart, as 2^(z c - r), r = rn(m c),
+// and one factor 2^(r - m c) for them all; one by one in the form above when m c is out of range.
+template <typename E, int kThreads>
+__device__ __forceinline__ void add_shared(Sum& sum, const uint4* src, int count, float c) {
+  constexpr int kPer = El<E>::kPerVec;
+  typename El<E>::Max most;
+#pragma unroll 4
+  for (int j = 0; j < count; ++j) most.add(src[j * kThreads]);
+  const float m = fmaxf(sum.m, most.value());
+  const float r = m * c;
+  if (!(fabsf(r) < 1e37f)) {
+#pragma unroll 1
+    for (int j = 0; j < count; ++j) {
+      const uint4 one[1] = {src[j * kThreads]};
+      add_vectors<E>(sum, one, c);
     }
-  const float2 t = unpair(add2(s[0], s[1]));
-  sum = Sum{m, t.x + t.y};
+    return;
+  }
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int j = 0; j < count; ++j) {
+    const uint4 d = src[j * kThreads];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s[i & 3] += ex2(fmaf(El<E>::get(d, i), c, -r));
+  }
+  const float before = sum.m == -INFINITY ? sum.s : sum.s * ex2((sum.m - m) * c);
+  sum = Sum{m, fmaf((s[0] + s[1]) + (s[2] + s[3]), ex2(fmaf(-m, c, r)), before)};
 }
 __device__ __forceinline__ void add_one(Sum& sum, float x, float c) {
   const float m = fmaxf(sum.m, x);
@@ -425,16 +485,21 @@ distill_warp_kernel(const DistillArgs a) {
     if constexpr (kMode != kFwd) {
       const bool zero = g == 0.0f || ls.m == -INFINITY;  // no gradient, whatever z holds
       const auto q = [&] {
-        if constexpr (kMode == kBwd) return grad_of(lse, g, c);
+        if constexpr (kMode == kBwd) return GradLse(lse, g, c);
         else return grad_of(sum, g, c);
       }();
       if (!zero) list_grad(list, a, q, g, lane, 32);
       E* out = static_cast<E*>(a.dz) + b * a.ld_d;
       const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
 #pragma unroll
-      for (int j = 0; j < kNV; ++j)
-        put_vector(out + row.head, j * 32 + lane, row.nvec, d[j], q, zero, same,
-                   s_stage + warp * 32, lane);
+      for (int j = 0; j < kNV; ++j) {
+        const int v = j * 32 + lane;
+        uint4* stage = s_stage + warp * 32;
+        if (zero)
+          put_vector<E, kZero>(out + row.head, v, row.nvec, d[j], q, same, stage, lane);
+        else
+          put_vector<E, kSlow>(out + row.head, v, row.nvec, d[j], q, same, stage, lane);
+      }
       if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
       __syncwarp();  // the listed columns' values replace those of the row
       if (!zero)
@@ -445,23 +510,36 @@ distill_warp_kernel(const DistillArgs a) {
   }
 }
 
-// kBwd: units of 8 vectors per thread, each by itself, in registers.
+// kBwd: units of 8 vectors per data thread, each by itself, in registers.  A list warp is a unit
+// ahead with the lists (two copies: a unit's is in use until the next unit's barrier).
 constexpr int kBwdVecs = 8;
 template <typename E>
-__global__ void __launch_bounds__(DTHREADS, 4)
+__global__ void __launch_bounds__(DTHREADS + 32, 3)
 distill_backward_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ uint4 s_stage[DTHREADS];
-  __shared__ Sum s_ls;
+  __shared__ Sum s_ls[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = kLog2e / a.T;
-  const List list(smem, a.kpad);
   const int64_t units = (int64_t)a.B << a.lsh;
-  ListLoader<E> loader;
-  if (warp == 0) loader.begin(a, blockIdx.x >> a.lsh, lane);
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+  auto list_at = [&](int i) { return List(smem + (size_t)i * kListBytes * a.kpad, a.kpad); };
+  auto slice_of = [&](int64_t unit) { return (int)(unit & ((1 << a.lsh) - 1)); };
+  if (warp == DWARPS) {
+    ListLoader<E> loader;
+    loader.begin(a, blockIdx.x >> a.lsh, lane);
+    int par = 0;
+    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, par ^= 1) {
+      const Sum ls = loader.end(list_at(par), a, unit >> a.lsh, c, lane, slice_of(unit) == 0);
+      if (lane == 0) s_ls[par] = ls;
+      if (unit + gridDim.x < units) loader.begin(a, (unit + gridDim.x) >> a.lsh, lane);
+      __syncthreads();
+    }
+    return;
+  }
+  int par = 0;
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, par ^= 1) {
     const int64_t b = unit >> a.lsh;
-    const int slice = (int)(unit & ((1 << a.lsh) - 1));
+    const int slice = slice_of(unit);
     const Row<E> row(a, b, slice, a.lsh, tid);
     uint4 d[kBwdVecs];
 #pragma unroll
@@ -471,59 +549,68 @@ distill_backward_kernel(const DistillArgs a) {
     }
     const float x = row.extra >= 0 ? El<E>::get(row.z[row.extra]) : -INFINITY;
     const float g = a.dloss[b] * a.T;
-    const Grad<true> q = grad_of(a.lse[b], g, c);
-    if (warp == 0) {
-      const Sum ls = loader.end(list, a, b, c, lane, slice == 0);
-      if (lane == 0) s_ls = ls;
-      if (unit + gridDim.x < units) loader.begin(a, (unit + gridDim.x) >> a.lsh, lane);
-    }
-    __syncthreads();
-    const bool zero = g == 0.0f || s_ls.m == -INFINITY;
+    const GradLse q(a.lse[b], g, c);
+    __syncthreads();  // the unit's list
+    const List list = list_at(par);
+    const bool zero = g == 0.0f || s_ls[par].m == -INFINITY;
     if (!zero) list_grad(list, a, q, g, tid, DTHREADS);
     E* out = static_cast<E*>(a.dz) + b * a.ld_d;
     const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
+    auto put = [&](auto form) {
 #pragma unroll
-    for (int j = 0; j < kBwdVecs; ++j)
-      put_vector(out + row.head, row.v0 + j * DTHREADS + tid, row.v1, d[j], q, zero, same,
-                 s_stage + warp * 32, lane);
+      for (int j = 0; j < kBwdVecs; ++j) {
+        const int v = row.v0 + j * DTHREADS + tid;
+        if (v - lane >= row.v1) break;
+        put_vector<E, decltype(form)::value>(out + row.head, v, row.v1, d[j], q, same,
+                                             s_stage + warp * 32, lane);
+      }
+    };
+    if (zero)
+      put(FormOf<kZero>());
+    else if (q.far)
+      put(FormOf<kSlow>());
+    else
+      put(FormOf<kFast>());
     if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
-    __syncthreads();  // the listed columns' values replace those of the row
+    // the listed columns' values replace those of the row
+    asm volatile("bar.sync 2, %0;" ::"n"(DTHREADS) : "memory");
     if (!zero)
       for (int j = tid; j < a.k; j += DTHREADS) {
         const int at = list.idx[j];
         if (at >= 0 && row.mine(at, slice)) El<E>::put(out + at, list.dz[j]);
       }
-    __syncthreads();  // the list and s_ls have been read
   }
 }
 
 // kFwd and kTrain: a CTA per slice of a row, a cluster per row.
-//   data warps  each chunk of the slice: maximum and sum (first pass); the slice's sums go to the
-//               cluster's other CTAs through shared memory (st.async); then (kTrain) each chunk
-//               again: the gradient, written out (second pass);
-//   list warp   the rows' lists; the loss, by the slices in turn;
+//   data warps  each chunk of the slice: maximum and sum (first pass); then (kTrain) each chunk
+//               again: the gradient, written out (second pass).  A vector is always the same
+//               warp's, so the warps need no barrier among themselves;
+//   list warps  (every other row each) join the data warps' sums and send them to the cluster's
+//               CTAs (st.async to shared memory), the rows' lists, the loss (by the slices in
+//               turn);
 //   copy warp   the slices' chunks by bulk copies into a ring of slots.
 // A row's second pass comes after the next row's first, so the exchange costs no waiting, and
 // in kTrain a slot is free when its gradient is written: the ring holds up to three rows'
 // slices, one in each pass and one on its way.
 //
-// Order.  Per row i there is one barrier of data and list warps, B(i), after its first pass and
-// its list.  Then a data thread sends the slice's sum, and:
-//   data warps  B(i), send i, second pass of i - 1, first pass of i + 1, B(i + 1), ...
-//   list warp   B(i), loss of i - 1, list of i + 1, B(i + 1), ...
-// - list i is in use until the second pass of i ends, before B(i + 2): three copies of a list;
-// - dz may be z: row i is written after every CTA of the cluster has sent its sum, so after
-//   every list warp has read row i;
-// - warps' sums i are read until B(i + 2), by the list warp: three copies;
-// - slices' sums i are read before B(i + 2), and another CTA sends its sum i + 4 after it has
-//   waited for this CTA's sum i + 2 (in its second pass of i + 2; in kFwd for that alone), sent
-//   after B(i + 2): four copies.
+// Order.  A data warp: first pass of i + 1, local(i + 1), wait sums(i), second pass of i.  A list
+// warp: list i, wait local(i), send i, list i + 2, wait sums(i), loss of i.  local(i): every data
+// warp's sum of row i is written; sums(i): every slice's sum of row i has come.  So
+// - local(i + 2) says that row i's second pass is over (here), sums(i + 2) that it is over or
+//   does not wait for anything of this CTA (elsewhere);
+// - dz may be z: row i is written after sums(i), so after every CTA has read list i;
+// - list i + 4 is loaded after local(i + 2), a warp's sum i + 4 is written after sums(i + 2), and
+//   another CTA sends i + 4 after its second pass of i + 2, for which this CTA sent i + 2 after
+//   its loss of i: four copies of each do.  In kFwd, without second passes, data warps wait for
+//   sums(i - 3) before they write their sum i, and list warps for sums(i - 2) before they send.
 constexpr int kCopies = 4;
 constexpr int kMaxSlots = 16;
 constexpr int kChunkVecs = 2048;        // 32 KB
 constexpr size_t kDynamic = 216 * 1024;  // dynamic shared memory at most
 constexpr int kTrainChunks = 2;  // of a slice, at most: two slices fit beside the longest lists
-static_assert(2 * kTrainChunks * 16 * kChunkVecs + 3 * kListBytes * PKM_DISTILL_MAX_K <= kDynamic,
+static_assert(2 * kTrainChunks * 16 * kChunkVecs + kCopies * kListBytes * PKM_DISTILL_MAX_K <=
+                  kDynamic,
               "ring of the longest slices");
 
 // What the data warps need of a row, written by the copy warp before the row's first chunk.
@@ -537,19 +624,21 @@ struct Geo {
   int same;  // z's and dz's rows start alike within 16 bytes
 };
 
-constexpr int kData = DWARPS;
+constexpr int kData = DWARPS, kListWarps = 2;
+constexpr int kStreamThreads = 32 * (kData + kListWarps + 1);
 template <typename E, int kMode>
-__global__ void __launch_bounds__(kData * 32 + 64, kMode == kTrain ? 2 : 3)
+__global__ void __launch_bounds__(kStreamThreads, kMode == kTrain ? 2 : 3)
 distill_stream_kernel(const DistillArgs a) {
   using namespace tc;
   constexpr int kThreads = kData * 32, kPer = El<E>::kPerVec;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint4 s_stage[kMode == kFwd ? 1 : kThreads];
-  __shared__ Sum s_warp[3][kData];
+  __shared__ Sum s_warp[kCopies][kData];
   __shared__ __align__(8) Sum s_slice[kCopies][kMaxSlices];
-  __shared__ Sum s_ls[3];
+  __shared__ float s_tm[kCopies];   // largest t of the list, -inf if it is empty
+  __shared__ int s_twice[kCopies];  // a column may occur twice in the list
   __shared__ __align__(16) Geo<E> s_geo[kCopies];
-  __shared__ __align__(8) uint64_t s_bars[2 * kMaxSlots + kCopies];
+  __shared__ __align__(8) uint64_t s_bars[2 * kMaxSlots + 2 * kCopies];
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = kLog2e / a.T;
@@ -561,18 +650,22 @@ distill_stream_kernel(const DistillArgs a) {
   const uint32_t bar0 = smem_u32(s_bars);
   auto bar_full = [&](int s) { return bar0 + 8u * s; };
   auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxSlots + s); };
-  auto bar_sums = [&](int i) { return bar0 + 8u * (2 * kMaxSlots + i); };
+  auto bar_sums = [&](int i) { return bar0 + 8u * (2 * kMaxSlots + i % kCopies); };
+  auto bar_local = [&](int i) { return bar0 + 8u * (2 * kMaxSlots + kCopies + i % kCopies); };
   if (tid == 0) {
     for (int s = 0; s < slots; ++s) {
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), kData);
     }
-    for (int i = 0; i < kCopies; ++i) mbar_init(bar_sums(i), 1);
+    for (int i = 0; i < kCopies; ++i) {
+      mbar_init(bar_sums(i), 1);
+      mbar_init(bar_local(i), kData);
+    }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  if (slices > 1) cluster_sync();  // every CTA's barriers exist before its memory is written
+  cluster_sync();  // every CTA's barriers exist before its memory is written
   const Ctl ctl{&s_abort, a.status};
 
   // this CTA's slice (consecutive CTAs, a cluster's, have those of one row) of rows first + i *
@@ -581,7 +674,7 @@ distill_stream_kernel(const DistillArgs a) {
   const int64_t first = blockIdx.x >> lsh, every = gridDim.x >> lsh;
   const int count = (int)((a.B - first + every - 1) / every);
   auto row_at = [&](int i) { return first + i * every; };
-  if (warp == kData + 1) {
+  if (warp == kData + kListWarps) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
       int s = 0, issued = 0;
@@ -624,39 +717,60 @@ distill_stream_kernel(const DistillArgs a) {
     }
     return;
   }
-  auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads + 32) : "memory"); };
   // the row's sum, once every slice's has come
-  auto sum_of = [&](int i) {
-    if (slices == 1) return lanes_join<kData>(s_warp[i % 3][lane & (kData - 1)], c);
-    wait_phase_cluster(bar_sums(i % kCopies), (uint32_t)(i / kCopies) & 1u, ctl);
+  auto wait_sums = [&](int i) {
+    wait_phase_cluster(bar_sums(i), (uint32_t)(i / kCopies) & 1u, ctl);
     __syncwarp();
+  };
+  auto sum_of = [&](int i) {
     return lanes_join<kMaxSlices>(lane % kMaxSlices < slices
                                       ? s_slice[i % kCopies][lane % kMaxSlices]
                                       : Sum{-INFINITY, 0.0f}, c);
   };
-  if (warp == kData) {
-    // ---------------------------------------------------------------- lists and losses
+  if (warp >= kData) {
+    // ---------------------------------------------------------------- lists, sums, losses
+    auto my_loss = [&](int i) { return (i / kListWarps & (slices - 1)) == slice; };
     // (kFwd needs a row's list for its loss alone)
-    auto wanted = [&](int i) {
-      return i < count && (kMode == kTrain || (i & (slices - 1)) == slice);
-    };
+    auto wanted = [&](int i) { return i < count && (kMode == kTrain || my_loss(i)); };
     ListLoader<E> loader;
-    auto list = [&](int i) {
-      if (!wanted(i)) return;
-      const Sum ls = loader.end(list_at(i % 3), a, row_at(i), c, lane, (i & (slices - 1)) == slice);
-      if (lane == 0) s_ls[i % 3] = ls;
+    Sum ls_next{-INFINITY, 0.0f};
+    auto load = [&](int i) {  // the list asked for before; asks for the one after it
+      if (wanted(i)) {
+        ls_next = loader.end(list_at(i % kCopies), a, row_at(i), c, lane, my_loss(i));
+        if (kMode == kTrain) {
+          const bool twice = list_at(i % kCopies).twice(a.kpad, lane);
+          if (lane == 0) s_tm[i % kCopies] = ls_next.m, s_twice[i % kCopies] = twice;
+        }
+      }
       __syncwarp();
+      if (wanted(i + kListWarps)) loader.begin(a, row_at(i + kListWarps), lane);
     };
-    if (wanted(0)) loader.begin(a, row_at(0), lane);
-    list(0);
-    if (wanted(1)) loader.begin(a, row_at(1), lane);
-    for (int i = 0; i <= count; ++i) {
-      if (i < count) meet();  // B(i)
-      if (i > 0 && ((i - 1) & (slices - 1)) == slice)
-        put_loss(a, row_at(i - 1), sum_of(i - 1), list_at((i - 1) % 3), s_ls[(i - 1) % 3], lane);
-      list(i + 1);
-      if (wanted(i + 2)) loader.begin(a, row_at(i + 2), lane);
+    const int h = warp - kData;
+    if (wanted(h)) loader.begin(a, row_at(h), lane);
+    load(h);
+    for (int i = h; i < count; i += kListWarps) {
+      const Sum ls = ls_next;
+      if (kMode == kFwd && i > 1) wait_sums(i - 2);
+      wait_phase(bar_local(i), (uint32_t)(i / kCopies) & 1u, ctl);
+      __syncwarp();
+      const Sum sum = lanes_join<kData>(s_warp[i % kCopies][lane & (kData - 1)], c);
+      // to every CTA of the cluster (this one too), completing on the receiver's barrier
+      if (lane == 0) mbar_expect_tx(bar_sums(i), 8u * slices);
+      if (lane < slices)
+        asm volatile(
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
+                "r"(mapa_shared(smem_u32(&s_slice[i % kCopies][slice]), lane)),
+            "r"(__float_as_uint(sum.m)), "r"(__float_as_uint(sum.s)),
+            "r"(mapa_shared(bar_sums(i), lane))
+            : "memory");
+      load(i + kListWarps);
+      if (my_loss(i)) {
+        wait_sums(i);
+        put_loss(a, row_at(i), sum_of(i), list_at(i % kCopies), ls, lane);
+      }
     }
+    // the other CTAs' last sums are here before this CTA's memory goes
+    for (int i = max(0, count - 2); i < count; ++i) wait_sums(i);
     return;
   }
   // ------------------------------------------------------------------ data
@@ -675,83 +789,90 @@ distill_stream_kernel(const DistillArgs a) {
       for (int v = 0;;) {
         const uint4* src = ring + (size_t)s1 * chunk + tid;
         const int n = min(chunk, total - v);
-        constexpr int kNV = kChunkVecs / kThreads;
-        uint4 d[kNV];
-#pragma unroll
-        for (int j = 0; j < kNV; ++j)
-          d[j] = j * kThreads + tid < n ? src[j * kThreads] : masked_vector<E>();
+        add_shared<E, kThreads>(sum, src, max(0, n - tid + kThreads - 1) / kThreads, c);
         if constexpr (kMode == kFwd) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_empty(s1));
         }
-        add_vectors<E>(sum, d, c);
         if (++s1 == slots) s1 = 0, ph ^= 1u;
         if ((v += chunk) >= total) break;
         wait_phase(bar_full(s1), ph, ctl);
       }
       if (geo.ends) add_one(sum, x, c);
       sum = lanes_join<32>(sum, c);
-      if (lane == 0) s_warp[i % 3][warp] = sum;
-      meet();  // B(i)
-      if (slices > 1 && warp == 0) {
-        if (kMode == kFwd && i > 1) sum_of(i - 2);
-        sum = lanes_join<kData>(s_warp[i % 3][lane & (kData - 1)], c);
-        const uint32_t bar = bar_sums(i % kCopies);
-        if (lane == 0) mbar_expect_tx(bar, 8u * slices);
-        if (lane < slices)
-          asm volatile(
-              "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, "
-              "[%3];" ::"r"(mapa_shared(smem_u32(&s_slice[i % kCopies][slice]), lane)),
-              "r"(__float_as_uint(sum.m)), "r"(__float_as_uint(sum.s)),
-              "r"(mapa_shared(bar, lane))
-              : "memory");
+      if (kMode == kFwd && i > 2) wait_sums(i - 3);
+      if (lane == 0) {
+        s_warp[i % kCopies][warp] = sum;
+        mbar_arrive(bar_local(i));
       }
     }
     if (kMode == kTrain && i > 0) {
       const Geo<E>& geo = s_geo[(i - 1) % kCopies];
-      const List list = list_at((i - 1) % 3);
+      const List list = list_at((i - 1) % kCopies);
       const float g = geo.g;
-      const bool zero = g == 0.0f || s_ls[(i - 1) % 3].m == -INFINITY;  // whatever z holds
-      const Grad<false> q = grad_of(sum_of(i - 1), g, c);
-      if (!zero) list_grad(list, a, q, g, tid, kThreads);
+      wait_sums(i - 1);
+      const bool zero = g == 0.0f || s_tm[(i - 1) % kCopies] == -INFINITY;  // whatever z holds
+      const Grad q = grad_of(sum_of(i - 1), g, c);
       E* body = geo.body;
       const int total = geo.n;
       const bool same = geo.same;
       for (int v = 0; v < total || v == 0; v += chunk) {
         const uint4* src = ring + (size_t)s2 * chunk;
         const int n = min(chunk, total - v);
-#pragma unroll
-        for (int j = 0; j < kChunkVecs / kThreads; ++j) {
-          const int at = j * kThreads + tid;
-          if (at - lane >= n) break;
-          put_vector(body + (int64_t)v * kPer, at, n, at < n ? src[at] : masked_vector<E>(), q, zero,
-                     same, s_stage + warp * 32, lane);
-        }
+        E* out = body + (int64_t)v * kPer;
+        auto put = [&](auto form) {
+          constexpr Form kForm = decltype(form)::value;
+          if (same) {
+#pragma unroll 4
+            for (int at = tid; at < n; at += kThreads)
+              put_vector<E, kForm>(out, at, n, src[at], q, true, nullptr, lane);
+          } else {
+            for (int at = tid; at - lane < n; at += kThreads)
+              put_vector<E, kForm>(out, at, n, at < n ? src[at] : masked_vector<E>(), q, false,
+                                   s_stage + warp * 32, lane);
+          }
+        };
+        if (zero)
+          put(FormOf<kZero>());
+        else if (q.far)
+          put(FormOf<kSlow>());
+        else
+          put(FormOf<kFast>());
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty(s2));
         if (++s2 == slots) s2 = 0;
       }
-      if (tid < geo.ends) {
-        E* out = body - ((int64_t)geo.v0 * kPer + geo.head);
+      E* out = body - ((int64_t)geo.v0 * kPer + geo.head);
+      if (tid < geo.ends)
         El<E>::put(out + (tid < geo.head ? tid : geo.nvec * kPer + tid), zero ? 0.0f : q(x_last));
-      }
-      // the listed columns' values replace those of the row
-      asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+      // this warp's listed columns: their values replace those of the row
+      __syncwarp();
       if (!zero) {
-        E* out = body - ((int64_t)geo.v0 * kPer + geo.head);
-        for (int j = tid; j < a.k; j += kThreads) {
-          const int at = list.idx[j];
-          if (at < 0) continue;
-          const bool outside = at < geo.head || at >= geo.head + geo.nvec * kPer;
+        const bool twice = s_twice[(i - 1) % kCopies];
+        for (int j0 = 0; j0 < a.k; j0 += 32) {
+          const int j = j0 + lane;
+          const int at = j < a.k ? list.idx[j] : -1;
           const int v = (at - geo.head) / kPer - geo.v0;
-          if (outside ? slice == 0 : v >= 0 && v < total) El<E>::put(out + at, list.dz[j]);
+          const bool outside = at < geo.head || at >= geo.head + geo.nvec * kPer;
+          const bool mine =
+              at >= 0 && (outside ? slice == 0 && warp == 0
+                                  : v >= 0 && v < total && (v & (kThreads - 1)) >> 5 == warp);
+          float p = mine ? list.p[j] : 0.0f;
+          if (twice && __any_sync(0xffffffffu, mine)) {
+            p = 0.0f;  // of every entry that names the column
+            if (mine)
+              for (int l = 0; l < a.kpad; l += 4) {
+                const int4 i4 = *reinterpret_cast<const int4*>(list.idx + l);
+                const float4 p4 = *reinterpret_cast<const float4*>(list.p + l);
+                p += (i4.x == at ? p4.x : 0.0f) + (i4.y == at ? p4.y : 0.0f) +
+                     (i4.z == at ? p4.z : 0.0f) + (i4.w == at ? p4.w : 0.0f);
+              }
+          }
+          if (mine) El<E>::put(out + at, fmaf(-g, p, q(list.z[j])));
         }
       }
     }
   }
-  // (the other CTAs' last sums may still be on their way here)
-  if (kMode == kFwd && slices > 1 && warp == 0)
-    for (int i = max(0, count - 2); i < count; ++i) sum_of(i);
 }
 
 // CTAs that run at one time at most, for a grid that leaves no second round to a few.
@@ -784,11 +905,11 @@ cudaError_t launch_backward(DistillArgs& a, cudaStream_t stream) {
   static int most = 0;
   auto kernel = distill_backward_kernel<E>;
   cudaError_t e =
-      resident_ctas(&most, kernel, DTHREADS, (size_t)PKM_DISTILL_MAX_K * kListBytes);
+      resident_ctas(&most, kernel, DTHREADS + 32, (size_t)2 * PKM_DISTILL_MAX_K * kListBytes);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.B << a.lsh;
-  kernel<<<(unsigned)(units < most ? units : most), DTHREADS, (size_t)kListBytes * a.kpad,
-           stream>>>(a);
+  kernel<<<(unsigned)(units < most ? units : most), DTHREADS + 32,
+           (size_t)2 * kListBytes * a.kpad, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -796,14 +917,14 @@ template <typename E, int kMode>
 cudaError_t launch_stream(const DistillArgs& a, cudaStream_t stream) {
   auto kernel = distill_stream_kernel<E, kMode>;
   const int slices = 1 << a.lsh;
-  const size_t smem = (size_t)a.slots * a.chunk * 16 + (size_t)3 * kListBytes * a.kpad;
+  const size_t smem = (size_t)a.slots * a.chunk * 16 + (size_t)kCopies * kListBytes * a.kpad;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = slices;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kData * 32 + 64);
+  cfg.blockDim = dim3(kStreamThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -849,7 +970,7 @@ cudaError_t dispatch_stream(DistillArgs& a, cudaStream_t stream) {
   if (a.chunk < 64) a.chunk = 64;
   const int64_t chunks = per ? (per + a.chunk - 1) / a.chunk : 1;
   const int64_t room =
-      (kDynamic - (size_t)3 * kListBytes * a.kpad) / ((size_t)a.chunk * 16);
+      (kDynamic - (size_t)kCopies * kListBytes * a.kpad) / ((size_t)a.chunk * 16);
   a.slots = kMode == kFwd ? 2 : (int)(chunks * 3 < room ? chunks * 3 : room);
   if (a.slots > kMaxSlots) a.slots = kMaxSlots;
   return launch_stream<E, kMode>(a, stream);
