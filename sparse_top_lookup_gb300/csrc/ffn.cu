@@ -14,10 +14,20 @@
 // the one before it is written out by eight epilogue warps.  Operands are
 // taken as they lie in memory: with K contiguous (K-major) or with M or N
 // contiguous (MN-major: the products with a transposed operand), both with
-// 128-byte swizzle.  What differs is the epilogue (Epi).
+// 128-byte swizzle.  What differs is the epilogue (Epi): each warp turns 32
+// columns of its 32 rows at a time into bf16 in its own shared-memory buffers
+// and stores them by TMA (a thread's own 64 bytes of a row, stored directly,
+// touch 32 lines per instruction: the gate's epilogue took longer than its
+// product that way).
+//
+// Work is split evenly over the clusters (Plan): whole tiles while there is
+// one for every cluster, then what is left in equal stretches of K slabs.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
+#include <chrono>
 
 #include "pkm_internal.cuh"
 #include "tc_common.cuh"
@@ -33,11 +43,12 @@ constexpr int FK = 64;                    // K per stage: one 128-byte swizzle r
 constexpr int FA_BYTES = FM * FK * 2;     // 16 KiB
 constexpr int FB_BYTES = FN / 2 * FK * 2; // 16 KiB: each CTA holds half of the columns
 constexpr int FSTAGE_BYTES = FA_BYTES + FB_BYTES;
-constexpr int FSTAGES = 6;
-constexpr int FSMEM = FSTAGES * FSTAGE_BYTES + 1024;  // + alignment slack
+constexpr int FSTAGES = 5;
 constexpr int FEPI_WARPS = 8;
+constexpr int FOUT_BYTES = 8192;          // of an epilogue warp: four buffers of 32 x 32 bf16
+constexpr int FSMEM = FSTAGES * FSTAGE_BYTES + FEPI_WARPS * FOUT_BYTES + 1024;  // + alignment
 constexpr int FTHREADS = 64 + 32 * FEPI_WARPS;
-static_assert(FSMEM <= 227 * 1024, "feed-forward shared memory");
+static_assert(FSMEM + 512 <= 227 * 1024, "feed-forward shared memory");
 
 enum Epi {
   kGate,    // accumulator columns: 128 of g, the same 128 of u; writes h (and g, u)
@@ -46,58 +57,122 @@ enum Epi {
   kDGate    // accumulator: dh; reads g, u; writes dg, du, h
 };
 
-// One launch: `groups` products of one shape that differ in A and C (group i:
-// a[i], b[i], c[i]), or one product whose K runs through `segs` pairs (a[i],
-// b[i]) one after the other.
+// How a launch's tiles are split over its clusters.  With T tiles of kb slabs and C clusters,
+// the first T / C * C tiles are done whole, one per cluster and round.  The slabs of the R tiles
+// left are laid end to end and cut into C stretches of w: a stretch begins with the end of a tile
+// (its cluster writes those sums to memory: a part) and goes on with the beginning of the next,
+// whose cluster adds the other stretches' parts, waits for them if it must, and writes the tile.
+// Stretches are done first, and a cluster waits only for clusters of lower numbers, which start
+// before it and never wait before they have written their part.
+struct Plan {
+  int tiles, kb, clusters;
+  int whole;   // tiles done whole
+  int w;       // slabs of a stretch, 0: no tile is cut (every tile is whole)
+};
+struct Seg {
+  int tile, k0, k1;
+  int part;    // >= 0: the sums go to this part instead of the tile
+  int parts;   // of the tile, to be added: [first, first + parts)
+  int first;
+};
+
+// One launch: `groups` products of one shape that differ in A and C (group i: a[i], b[i],
+// out[i]), or one product whose K runs through `segs` pairs (a[i], b[i]) one after the other.
 struct GemmArgs {
   CUtensorMap a[2], b[2];
-  int M, N, K;        // of one product; K of one segment
-  int segs, groups;   // at most one of them above 1
-  int a_mn, b_mn;     // operand stored with M (N) contiguous
-  int act;
-  void* c[2];                       // kStore: bf16 [M, N]; kAdd32: fp32 [M, N]
-  __nv_bfloat16 *g, *u, *h;         // kGate: written (g, u may be NULL)
-  const __nv_bfloat16 *g_in, *u_in; // kDGate
-  __nv_bfloat16 *dg, *du;
+  CUtensorMap out[3];  // kGate: h, g, u; kStore, kAdd32: by group; kDGate: dg, du, h
+  int M, N, K;         // of one product; K of one segment
+  int segs, groups;    // at most one of them above 1
+  int a_mn, b_mn;      // operand stored with M (N) contiguous
+  int act, keep;       // keep: kGate writes g and u
+  Plan plan;
+  const __nv_bfloat16 *g_in, *u_in;  // kDGate
+  float4* parts;                // [stretch][CTA of the pair][column / 4][row], part_rows rows
+  int part_rows;
+  unsigned long long* flags;    // [stretch][CTA of the pair][epilogue warp]
+  unsigned long long epoch;     // a flag's value when its part is there
   int* status;
 };
 
-__device__ __forceinline__ float act_fwd(float g, int act) {
-  switch (act) {
-    case PKM_ACT_SILU:
-      return __fdividef(g, 1.0f + __expf(-g));
-    case PKM_ACT_GELU:
-      return 0.5f * g * (1.0f + erff(g * 0.70710678f));
-    case PKM_ACT_GELU_TANH: {
-      // 0.5 (1 + tanh v) = 1 / (1 + exp(-2 v))
-      const float v2 = 1.59576912f * g * fmaf(0.044715f * g, g, 1.0f);
-      return __fdividef(g, 1.0f + __expf(-v2));
+// Segment i of cluster c; false past the last.
+__device__ __forceinline__ bool seg_at(const Plan& p, int c, int i, Seg& s) {
+  s.part = -1, s.parts = 0, s.first = 0;
+  if (p.w) {
+    const int r = p.clusters - 1 - c;  // a tile's later stretches belong to lower clusters
+    const int total = (p.tiles - p.whole) * p.kb;
+    const int lo = min(r * p.w, total), hi = min(lo + p.w, total);
+    const int t0 = lo / p.kb;
+    const int mid = lo == t0 * p.kb ? lo : min(hi, (t0 + 1) * p.kb);  // where a tile begins
+    const int n = (lo < mid) + (mid < hi);
+    if (i < n) {
+      if (i == 0 && lo < mid) {
+        s.tile = p.whole + t0, s.k0 = lo - t0 * p.kb, s.k1 = mid - t0 * p.kb, s.part = r;
+      } else {
+        const int t = mid / p.kb;
+        s.tile = p.whole + t, s.k0 = 0, s.k1 = hi - mid;
+        s.first = r + 1;
+        s.parts = ((t + 1) * p.kb - 1) / p.w - r;
+      }
+      return true;
     }
-    default:
-      return fmaxf(g, 0.0f);
+    i -= n;
   }
+  s.tile = c + i * p.clusters, s.k0 = 0, s.k1 = p.kb;
+  return s.tile < p.whole;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + exp(-x)), with x log2(e) given
+__device__ __forceinline__ float sigmoid2(float x2) { return rcp(1.0f + ex2(-x2)); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi): (1 + tanh v) / 2 = sigmoid(2 v)
+
 // act(g) and act'(g)
-__device__ __forceinline__ float2 act_both(float g, int act) {
-  switch (act) {
-    case PKM_ACT_SILU: {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-g));
-      return make_float2(g * s, s * fmaf(g, 1.0f - s, 1.0f));
-    }
-    case PKM_ACT_GELU: {
-      const float cdf = 0.5f * (1.0f + erff(g * 0.70710678f));
-      return make_float2(g * cdf, fmaf(g * 0.39894228f, __expf(-0.5f * g * g), cdf));
-    }
-    case PKM_ACT_GELU_TANH: {
-      const float g2 = g * g;
-      const float s = __fdividef(1.0f, 1.0f + __expf(-1.59576912f * g * fmaf(0.044715f, g2, 1.0f)));
-      return make_float2(g * s, s * fmaf(g * (1.0f - s), 1.59576912f * fmaf(0.134145f, g2, 1.0f),
-                                         1.0f));
-    }
-    default:
-      return make_float2(fmaxf(g, 0.0f), g > 0.0f ? 1.0f : 0.0f);
+template <int kAct>
+__device__ __forceinline__ float2 act_both(float g) {
+  if constexpr (kAct == PKM_ACT_SILU) {
+    const float s = sigmoid2(g * kLog2e), a = g * s;
+    return make_float2(a, fmaf(a, 1.0f - s, s));
+  } else if constexpr (kAct == PKM_ACT_GELU) {
+    const float cdf = 0.5f * (1.0f + erff(g * 0.70710678f));
+    return make_float2(g * cdf, fmaf(g * 0.39894228f, ex2(g * g * (-0.5f * kLog2e)), cdf));
+  } else if constexpr (kAct == PKM_ACT_GELU_TANH) {
+    const float g2 = g * g;
+    const float s = sigmoid2(kTanh * kLog2e * g * fmaf(0.044715f, g2, 1.0f)), a = g * s;
+    return make_float2(a, fmaf(a * (1.0f - s), kTanh * fmaf(0.134145f, g2, 1.0f), s));
+  } else {
+    return make_float2(fmaxf(g, 0.0f), g > 0.0f ? 1.0f : 0.0f);
   }
+}
+template <int kAct>
+__device__ __forceinline__ float act_fwd(float g) {
+  return act_both<kAct>(g).x;
+}
+// f(std::integral_constant-like tag) for the activation of a launch
+template <int kAct>
+struct ActTag {
+  static constexpr int value = kAct;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == PKM_ACT_SILU)
+    f(ActTag<PKM_ACT_SILU>());
+  else if (act == PKM_ACT_GELU)
+    f(ActTag<PKM_ACT_GELU>());
+  else if (act == PKM_ACT_GELU_TANH)
+    f(ActTag<PKM_ACT_GELU_TANH>());
+  else
+    f(ActTag<PKM_ACT_RELU>());
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -107,25 +182,71 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// 32 columns from column c0 of a row of an [., N] bf16 matrix (N a multiple of 8).
-__device__ __forceinline__ void store32(__nv_bfloat16* row, int c0, int N, const float (&v)[32]) {
+// A 32 x 32 block in shared memory as TMA stores it: rows of 64 bytes (bf16, 64-byte swizzle) or
+// of 128 (fp32, 128-byte swizzle); 16-byte piece `piece` of row `row`.
+__device__ __forceinline__ uint32_t at64(uint32_t buf, int row, int piece) {
+  return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t at128(uint32_t buf, int row, int piece) {
+  return buf + row * 128 + ((piece ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void sts(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Row `lane` of a block from 32 values.
+__device__ __forceinline__ void put_row(uint32_t buf, int lane, const float (&v)[32]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (c0 + 8 * j < N)
-      *reinterpret_cast<uint4*>(row + c0 + 8 * j) =
-          make_uint4(pack2(v[8 * j], v[8 * j + 1]), pack2(v[8 * j + 2], v[8 * j + 3]),
-                     pack2(v[8 * j + 4], v[8 * j + 5]), pack2(v[8 * j + 6], v[8 * j + 7]));
+    sts(at64(buf, lane, j),
+        make_uint4(pack2(v[8 * j], v[8 * j + 1]), pack2(v[8 * j + 2], v[8 * j + 3]),
+                   pack2(v[8 * j + 4], v[8 * j + 5]), pack2(v[8 * j + 6], v[8 * j + 7])));
 }
-__device__ __forceinline__ void load32(const __nv_bfloat16* row, int c0, int N, float (&v)[32]) {
+__device__ __forceinline__ void get_row(uint32_t buf, int lane, float (&v)[32]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (c0 + 8 * j < N) x = __ldg(reinterpret_cast<const uint4*>(row + c0 + 8 * j));
+    const uint4 x = lds(at64(buf, lane, j));
     v[8 * j] = lo_bf16(x.x), v[8 * j + 1] = hi_bf16(x.x);
     v[8 * j + 2] = lo_bf16(x.y), v[8 * j + 3] = hi_bf16(x.y);
     v[8 * j + 4] = lo_bf16(x.z), v[8 * j + 5] = hi_bf16(x.z);
     v[8 * j + 6] = lo_bf16(x.w), v[8 * j + 7] = hi_bf16(x.w);
   }
+}
+// A block's store (one thread), each in a group of its own.
+__device__ __forceinline__ void store_block(const CUtensorMap* map, uint32_t buf, int col, int row) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(col), "r"(row), "r"(buf)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void add_block(const CUtensorMap* map, uint32_t buf, int col, int row) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(col), "r"(row), "r"(buf)
+      : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the last kPending stores of this thread have read their blocks.
+template <int kPending>
+__device__ __forceinline__ void blocks_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ void blocks_written() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void blocks_visible() {  // this thread's writes, to the stores
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // Tile t of `groups` x (tm_count x tn_count): bands of 8 row tiles, within a
@@ -153,11 +274,8 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   constexpr int kTileN = kEpi == kGate ? FN / 2 : FN;  // output columns per tile
   const int tm_count = (p.M + 2 * FM - 1) / (2 * FM), tn_count = (p.N + kTileN - 1) / kTileN;
   const uint32_t rank = cluster_ctarank();
-  const int slot = (int)(blockIdx.x >> 1), slots = (int)(gridDim.x >> 1);
-  const int tiles = tm_count * tn_count * p.groups;
-  const int mine = slot < tiles ? (tiles - 1 - slot) / slots + 1 : 0;
-  if (mine == 0) return;  // both CTAs of the cluster alike
-  const int kb_seg = (p.K + FK - 1) / FK, kb_count = kb_seg * p.segs;
+  const int slot = (int)(blockIdx.x >> 1);
+  const int kb_seg = (p.K + FK - 1) / FK;
 
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -203,13 +321,14 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int i = 0; ok && i < mine; ++i) {
+      Seg sg;
+      for (int i = 0; ok && seg_at(p.plan, slot, i, sg); ++i) {
         int grp, tm, tn;
-        tile_at(slot + i * slots, tm_count, tn_count, grp, tm, tn);
+        tile_at(sg.tile, tm_count, tn_count, grp, tm, tn);
         const int row0 = (2 * tm + (int)rank) * FM;
         // kGate: CTA 0 holds the tile's rows of Wg, CTA 1 those of Wu
         const int col0 = kEpi == kGate ? tn * kTileN : tn * FN + (int)rank * (FN / 2);
-        for (int kb = 0; kb < kb_count; ++kb, ++it) {
+        for (int kb = sg.k0; kb < sg.k1; ++kb, ++it) {
           const uint32_t s = it % FSTAGES, ph = (it / FSTAGES) & 1u;
           if (!wait_phase_cluster(bar_empty(s), ph ^ 1u, ctl)) {
             ok = false;
@@ -252,11 +371,12 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
       uint32_t it = 0;
       bool ok = true;
-      for (int i = 0; ok && i < mine; ++i) {
+      Seg sg;
+      for (int i = 0; ok && seg_at(p.plan, slot, i, sg); ++i) {
         const uint32_t buf = i & 1u, use = i >> 1;
         if (!wait_phase_cluster(bar_tempty(buf), (use & 1u) ^ 1u, ctl)) break;
         tc_fence_after();
-        for (int kb = 0; kb < kb_count; ++kb, ++it) {
+        for (int kb = sg.k0; kb < sg.k1; ++kb, ++it) {
           const uint32_t s = it % FSTAGES, ph = (it / FSTAGES) & 1u;
           if (!wait_phase_cluster(bar_full(s), ph, ctl)) {
             ok = false;
@@ -270,7 +390,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
 #pragma unroll
           for (int kk = 0; kk < FK / 16; ++kk)
             tc_mma_cg2(tmem + buf * FN, a_desc + a_step * kk, b_desc + b_step * kk, idesc,
-                       (kb | kk) != 0);
+                       kb != sg.k0 || kk != 0);
           tc_commit_cg2_mc(bar_empty(s), 3);  // the stage is free again in both CTAs
         }
         if (!ok) break;
@@ -282,71 +402,210 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
     }
   } else {
     // ------------------------------------------------ epilogue (both CTAs)
-    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int quad = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    for (int i = 0; i < mine; ++i) {
+    const uint32_t bufs = stages_u32 + FSTAGES * FSTAGE_BYTES + ew * FOUT_BYTES;
+    uint32_t nb = 0;  // next buffer (of four; of two for fp32 blocks)
+    Seg sg;
+    for (int i = 0; seg_at(p.plan, slot, i, sg); ++i) {
       int grp, tm, tn;
-      tile_at(slot + i * slots, tm_count, tn_count, grp, tm, tn);
+      tile_at(sg.tile, tm_count, tn_count, grp, tm, tn);
       const uint32_t buf = i & 1u, use = i >> 1;
+      const uint32_t taddr = lane_addr + buf * FN;
+      const int row0 = (2 * tm + (int)rank) * FM + quad * 32;  // of the warp
+      const int row = row0 + lane;
+      constexpr int kHalfN = kTileN / 2;
+      const int cols = min(kHalfN, p.N - tn * kTileN - half * kHalfN);  // may be <= 0
+      const int col0 = tn * kTileN + half * kHalfN;
+      const bool in = row < p.M;
+      // this thread's part of a stretch's sums: [column / 4][row]
+      const int prow = quad * 32 + lane;
+      auto part_at = [&](int r) {
+        return p.parts + ((size_t)(2 * r + rank) * (FN / 4)) * p.part_rows + prow;
+      };
+      auto flag_at = [&](int r) { return p.flags + (size_t)(2 * r + rank) * FEPI_WARPS + ew; };
+
+      // kDGate: 16-byte pieces of g and u, four lanes to a row, asked for a chunk ahead
+      uint4 pg[kEpi == kDGate ? 4 : 1], pu[kEpi == kDGate ? 4 : 1];
+      auto ask = [&](int c) {
+        if constexpr (kEpi == kDGate) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = row0 + 8 * j + (lane >> 2), cc = c + 8 * (lane & 3);
+            pg[j] = pu[j] = make_uint4(0, 0, 0, 0);
+            if (r < p.M && cc < cols) {
+              const size_t at = (size_t)r * p.N + col0 + cc;
+              pg[j] = __ldcs(reinterpret_cast<const uint4*>(p.g_in + at));
+              pu[j] = __ldcs(reinterpret_cast<const uint4*>(p.u_in + at));
+            }
+          }
+        }
+      };
+      if (kEpi == kDGate && sg.part < 0) {
+        if (in)  // the rest of the tile into L2 meanwhile (128 bytes at a time)
+          for (int c = 64; c < cols; c += 64) {
+            const size_t at = (size_t)row * p.N + col0 + c;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.g_in + at));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.u_in + at));
+          }
+        ask(0);
+      }
       if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_tfull(buf), use & 1u, ctl))) break;
       tc_fence_after();
-      const uint32_t taddr = lane_addr + buf * FN;
-      const int row = (2 * tm + (int)rank) * FM + quad * 32 + lane;
-      const size_t at = (size_t)row * p.N;
-      constexpr int kHalfN = kTileN / 2;
-      for (int c = half * kHalfN; c < (half + 1) * kHalfN; c += 32) {
-        const int c0 = tn * kTileN + c;
-        if (c0 >= p.N) break;
-        float v[32];
-        tmem_ld32(taddr + c, v);
-        if constexpr (kEpi == kGate) {
-          float w[32];
-          tmem_ld32(taddr + FN / 2 + c, w);
-          if (row < p.M) {
-            if (p.g) {
-              store32(p.g + at, c0, p.N, v);
-              store32(p.u + at, c0, p.N, w);
+      if (row0 < p.M && cols > 0) {
+        if (sg.part >= 0) {
+          float4* dst = part_at(sg.part);
+          for (int c = 0; c < cols; c += 32) {
+#pragma unroll
+            for (int q = 0; q < (kEpi == kGate ? 2 : 1); ++q) {
+              const int tc = half * kHalfN + c + q * (FN / 2);
+              float v[32];
+              tmem_ld32(taddr + tc, v);
+              if (in)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  __stcg(dst + (size_t)(tc / 4 + j) * p.part_rows,
+                         make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] *= act_fwd(v[j], p.act);
-            store32(p.h + at, c0, p.N, w);
           }
-        } else if constexpr (kEpi == kStore) {
-          if (row < p.M) store32(static_cast<__nv_bfloat16*>(p.c[grp]) + at, c0, p.N, v);
-        } else if constexpr (kEpi == kAdd32) {
-          if (row < p.M) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.c[grp]) + at + c0);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (c0 + 4 * j < p.N) {
-                float4 t = dst[j];
-                t.x += v[4 * j], t.y += v[4 * j + 1], t.z += v[4 * j + 2], t.w += v[4 * j + 3];
-                dst[j] = t;
-              }
-          }
+          __threadfence();
+          __syncwarp();
+          if (lane == 0)
+            asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(flag_at(sg.part)), "l"(p.epoch)
+                         : "memory");
         } else {
-          if (row < p.M) {
-            float g[32], u[32];
-            load32(p.g_in + at, c0, p.N, g);
-            load32(p.u_in + at, c0, p.N, u);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 a = act_both(g[j], p.act);
-              g[j] = v[j] * u[j] * a.y;
-              u[j] *= a.x;  // h
-              v[j] *= a.x;  // du
+          for (int r = sg.first; r < sg.first + sg.parts; ++r) {
+            if (lane == 0) {
+              const unsigned long long t0 = globaltimer();
+              unsigned long long f;
+              do {
+                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(f) : "l"(flag_at(r))
+                             : "memory");
+                if (f != p.epoch && globaltimer() - t0 > WAIT_LIMIT_NS) {
+                  s_abort = 1;
+                  atomicExch(p.status, PKM_ERR_TIMEOUT);
+                  break;
+                }
+              } while (f != p.epoch && !*ctl.abort);
+              *flag_at(r) = 0;  // the next launch with this workspace starts afresh
             }
-            store32(p.dg + at, c0, p.N, g);
-            store32(p.du + at, c0, p.N, v);
-            store32(p.h + at, c0, p.N, u);
+            __syncwarp();
+          }
+          // accumulator columns tc .. tc + 31, with the other stretches' parts
+          auto sums = [&](int tc, float (&v)[32]) {
+            tmem_ld32(taddr + tc, v);
+            for (int r = sg.first; r < sg.first + sg.parts; ++r) {
+              const float4* src = part_at(r);
+              if (in)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const float4 t = __ldcg(src + (size_t)(tc / 4 + j) * p.part_rows);
+                  v[4 * j] += t.x, v[4 * j + 1] += t.y, v[4 * j + 2] += t.z, v[4 * j + 3] += t.w;
+                }
+            }
+          };
+          auto next_buf = [&] {
+            const uint32_t b = bufs + nb * 2048;
+            nb = (nb + 1) & 3;
+            return b;
+          };
+          for (int c = 0; c < cols; c += 32) {
+            const int tc = half * kHalfN + c, gc = col0 + c;
+            float v[32];
+            if constexpr (kEpi == kGate) {
+              float w[32];
+              sums(tc, v);
+              sums(FN / 2 + tc, w);
+              if (lane == 0) blocks_read<1>();
+              __syncwarp();
+              const uint32_t b0 = next_buf();
+              uint32_t b1 = 0, b2 = 0;
+              if (p.keep) {
+                b1 = next_buf(), b2 = next_buf();
+                put_row(b1, lane, v);
+                put_row(b2, lane, w);
+              }
+              with_act(p.act, [&](auto tag) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) w[j] *= act_fwd<decltype(tag)::value>(v[j]);
+              });
+              put_row(b0, lane, w);
+              blocks_visible();
+              __syncwarp();
+              if (lane == 0) {
+                store_block(&p.out[0], b0, gc, row0);
+                if (p.keep) {
+                  store_block(&p.out[1], b1, gc, row0);
+                  store_block(&p.out[2], b2, gc, row0);
+                }
+              }
+            } else if constexpr (kEpi == kStore) {
+              sums(tc, v);
+              if (lane == 0) blocks_read<3>();
+              __syncwarp();
+              const uint32_t b0 = next_buf();
+              put_row(b0, lane, v);
+              blocks_visible();
+              __syncwarp();
+              if (lane == 0) store_block(&p.out[grp], b0, gc, row0);
+            } else if constexpr (kEpi == kAdd32) {
+              sums(tc, v);
+              if (lane == 0) blocks_read<1>();
+              __syncwarp();
+              const uint32_t b0 = bufs + (nb & 1) * 4096;
+              ++nb;
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                sts(at128(b0, lane, j),
+                    make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                               __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+              blocks_visible();
+              __syncwarp();
+              if (lane == 0) add_block(&p.out[grp], b0, gc, row0);
+            } else {
+              if (lane == 0) blocks_read<1>();
+              __syncwarp();
+              const uint32_t b0 = next_buf(), b1 = next_buf(), b2 = next_buf();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                sts(at64(b0, 8 * j + (lane >> 2), lane & 3), pg[j]);
+                sts(at64(b1, 8 * j + (lane >> 2), lane & 3), pu[j]);
+              }
+              if (c + 32 < cols) ask(c + 32);
+              sums(tc, v);
+              __syncwarp();
+              float g[32], u[32];
+              get_row(b0, lane, g);
+              get_row(b1, lane, u);
+              with_act(p.act, [&](auto tag) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  const float2 a = act_both<decltype(tag)::value>(g[j]);
+                  g[j] = v[j] * u[j] * a.y;  // dg
+                  v[j] *= a.x;               // du
+                  u[j] *= a.x;               // h
+                }
+              });
+              put_row(b0, lane, g);
+              put_row(b1, lane, v);
+              put_row(b2, lane, u);
+              blocks_visible();
+              __syncwarp();
+              if (lane == 0) {
+                store_block(&p.out[0], b0, gc, row0);
+                store_block(&p.out[1], b1, gc, row0);
+                store_block(&p.out[2], b2, gc, row0);
+              }
+            }
           }
         }
       }
-      // tile written: hand the TMEM buffer back to the leader's MMA warp
+      // tile read: hand the TMEM buffer back to the leader's MMA warp
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(bar_tempty(buf), 0));
     }
+    if (lane == 0) blocks_written();
   }
 
   tc_fence_before();
@@ -377,9 +636,51 @@ bool encode2(CUtensorMap* m, const void* ptr, int rows, int cols, int box_cols, 
 bool operand(CUtensorMap* m, const void* ptr, int rows, int cols, bool mn) {
   return encode2(m, ptr, rows, cols, 64, mn ? FK : FM);
 }
+// A result [rows, cols] in blocks of 32 x 32, bf16 or fp32.
+bool result(CUtensorMap* m, void* ptr, int rows, int cols, bool f32 = false) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr,
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Parts of cut tiles, of products with at most M rows: [cluster][2][FN / 4][rows] float4, and
+// their flags.
+constexpr int kMaxClusters = 80;
+int part_rows(int M) { return M >= FM ? FM : (M + 31) / 32 * 32; }
+size_t parts_bytes(int M) {
+  return align256((size_t)kMaxClusters * 2 * FN * part_rows(M) * 4) +
+         align256((size_t)kMaxClusters * 2 * FEPI_WARPS * 8);
+}
+void set_parts(GemmArgs& p, void* ws, int M) {
+  p.part_rows = part_rows(M);
+  p.parts = static_cast<float4*>(ws);
+  p.flags = reinterpret_cast<unsigned long long*>(
+      static_cast<unsigned char*>(ws) +
+      align256((size_t)kMaxClusters * 2 * FN * p.part_rows * 4));
+}
+
+// The value of this launch's flags.  The workspace is whatever its memory held before: a flag
+// counts only if it has the launch's own 64-bit number, and is cleared when it has been seen (so
+// a captured launch can be replayed).
+unsigned long long next_epoch() {
+  static std::atomic<unsigned long long> n(
+      (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() *
+      0x9E3779B97F4A7C15ull);
+  const unsigned long long e = n.fetch_add(1, std::memory_order_relaxed);
+  return e ? e : n.fetch_add(1, std::memory_order_relaxed);
+}
 
 template <int kEpi>
-cudaError_t launch_gemm(const GemmArgs& p, cudaStream_t stream) {
+cudaError_t launch_gemm(GemmArgs& p, cudaStream_t stream) {
   auto kernel = ffn_gemm_kernel<kEpi>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -402,21 +703,45 @@ cudaError_t launch_gemm(const GemmArgs& p, cudaStream_t stream) {
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
-    max_clusters = n;
+    max_clusters = n < kMaxClusters ? n : kMaxClusters;
   }
   const int tile_n = kEpi == kGate ? FN / 2 : FN;
-  const int64_t tiles =
-      (int64_t)((p.M + 2 * FM - 1) / (2 * FM)) * ((p.N + tile_n - 1) / tile_n) * p.groups;
-  cfg.gridDim = dim3(2 * (unsigned)(tiles < max_clusters ? tiles : max_clusters));
+  Plan& pl = p.plan;
+  pl.tiles = (p.M + 2 * FM - 1) / (2 * FM) * ((p.N + tile_n - 1) / tile_n) * p.groups;
+  pl.kb = (p.K + FK - 1) / FK * p.segs;
+  pl.clusters = max_clusters;
+  pl.whole = pl.tiles / max_clusters * max_clusters;
+  const int left = pl.tiles - pl.whole;
+  pl.w = 0;
+  if (left) {
+    // Cutting pays when a stretch is shorter than a tile by more than its part costs to write
+    // and to read back, in slabs: about 3, and 8 more for all rows of a tile.
+    const int64_t slabs = (int64_t)left * pl.kb;
+    const int cost = 3 + 8 * (p.M < 2 * FM ? p.M : 2 * FM) / (2 * FM);
+    int64_t w = (slabs + max_clusters - 1) / max_clusters;
+    if (w < 2) w = 2;  // (fewer clusters, but each with something in flight)
+    if (w + cost < pl.kb && slabs < INT32_MAX / 2)
+      pl.w = (int)w;
+    else
+      pl.whole = pl.tiles;
+  }
+  if (pl.w && !pl.whole)  // fewer stretches than clusters
+    pl.clusters = (int)(((int64_t)left * pl.kb + pl.w - 1) / pl.w);
+  else if (!pl.w && pl.tiles < max_clusters)
+    pl.clusters = pl.tiles;
+  p.epoch = next_epoch();
+  cfg.gridDim = dim3(2 * (unsigned)pl.clusters);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-
 }  // namespace
 
-size_t gated_ffn_workspace_bytes(int B, int F) { return align256((size_t)B * F * 2); }
-size_t gated_ffn_backward_workspace_bytes(int B, int F) { return 3 * align256((size_t)B * F * 2); }
+size_t gated_ffn_workspace_bytes(int B, int F) {
+  return align256((size_t)B * F * 2) + parts_bytes(B);
+}
+size_t gated_ffn_backward_workspace_bytes(int B, int F) {
+  return 3 * align256((size_t)B * F * 2) + parts_bytes(FM);
+}
 
 cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up,
                              const void* w_down, int B, int dim, int F, int act, void* workspace,
@@ -426,17 +751,17 @@ cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up
   p.act = act;
   p.status = status;
   p.M = B, p.N = F, p.K = dim;
-  p.g = static_cast<__nv_bfloat16*>(gate);
-  p.u = static_cast<__nv_bfloat16*>(up);
-  p.h = static_cast<__nv_bfloat16*>(workspace);
+  p.keep = gate != nullptr;
+  set_parts(p, static_cast<unsigned char*>(workspace) + align256((size_t)B * F * 2), B);
   if (!operand(&p.a[0], x, B, dim, false) || !operand(&p.b[0], w_gate, F, dim, false) ||
-      !operand(&p.b[1], w_up, F, dim, false))
+      !operand(&p.b[1], w_up, F, dim, false) || !result(&p.out[0], workspace, B, F) ||
+      (gate && (!result(&p.out[1], gate, B, F) || !result(&p.out[2], up, B, F))))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_gemm<kGate>(p, stream);
   if (e != cudaSuccess) return e;
   p.N = dim, p.K = F;
-  p.c[0] = y;
-  if (!operand(&p.a[0], workspace, B, F, false) || !operand(&p.b[0], w_down, dim, F, false))
+  if (!operand(&p.a[0], workspace, B, F, false) || !operand(&p.b[0], w_down, dim, F, false) ||
+      !result(&p.out[0], y, B, dim))
     return cudaErrorInvalidValue;
   return launch_gemm<kStore>(p, stream);
 }
@@ -449,26 +774,26 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
                                       cudaStream_t stream) {
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const size_t part = align256((size_t)B * F * 2);
+  void *dg = ws, *du = ws + part, *h = ws + 2 * part;
   GemmArgs p = {};
   p.segs = p.groups = 1;
   p.act = act;
   p.status = status;
   p.g_in = static_cast<const __nv_bfloat16*>(gate);
   p.u_in = static_cast<const __nv_bfloat16*>(up);
-  p.dg = reinterpret_cast<__nv_bfloat16*>(ws);
-  p.du = reinterpret_cast<__nv_bfloat16*>(ws + part);
-  p.h = reinterpret_cast<__nv_bfloat16*>(ws + 2 * part);
+  set_parts(p, ws + 3 * part, FM);
   // dh = dy Wd, then dg, du and h
   p.M = B, p.N = F, p.K = dim, p.b_mn = 1;
-  if (!operand(&p.a[0], dy, B, dim, false) || !operand(&p.b[0], w_down, dim, F, true))
+  if (!operand(&p.a[0], dy, B, dim, false) || !operand(&p.b[0], w_down, dim, F, true) ||
+      !result(&p.out[0], dg, B, F) || !result(&p.out[1], du, B, F) || !result(&p.out[2], h, B, F))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_gemm<kDGate>(p, stream);
   if (e != cudaSuccess) return e;
   if (dx) {  // dx = dg Wg + du Wu: one product of twice the depth
     p.N = dim, p.K = F, p.segs = 2;
-    p.c[0] = dx;
-    if (!operand(&p.a[0], p.dg, B, F, false) || !operand(&p.a[1], p.du, B, F, false) ||
-        !operand(&p.b[0], w_gate, F, dim, true) || !operand(&p.b[1], w_up, F, dim, true))
+    if (!operand(&p.a[0], dg, B, F, false) || !operand(&p.a[1], du, B, F, false) ||
+        !operand(&p.b[0], w_gate, F, dim, true) || !operand(&p.b[1], w_up, F, dim, true) ||
+        !result(&p.out[0], dx, B, dim))
       return cudaErrorInvalidValue;
     if ((e = launch_gemm<kStore>(p, stream)) != cudaSuccess) return e;
     p.segs = 1;
@@ -477,9 +802,9 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
   p.a_mn = 1, p.K = B;
   if (dw_gate) {  // dWg = dg^T x and dWu = du^T x
     p.M = F, p.N = dim, p.groups = 2;
-    p.c[0] = dw_gate, p.c[1] = dw_up;
-    if (!operand(&p.a[0], p.dg, B, F, true) || !operand(&p.a[1], p.du, B, F, true) ||
-        !operand(&p.b[0], x, B, dim, true))
+    if (!operand(&p.a[0], dg, B, F, true) || !operand(&p.a[1], du, B, F, true) ||
+        !operand(&p.b[0], x, B, dim, true) || !result(&p.out[0], dw_gate, F, dim, add) ||
+        !result(&p.out[1], dw_up, F, dim, add))
       return cudaErrorInvalidValue;
     p.b[1] = p.b[0];
     e = add ? launch_gemm<kAdd32>(p, stream) : launch_gemm<kStore>(p, stream);
@@ -488,8 +813,8 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
   }
   if (dw_down) {  // dWd = dy^T h
     p.M = dim, p.N = F;
-    p.c[0] = dw_down;
-    if (!operand(&p.a[0], dy, B, dim, true) || !operand(&p.b[0], p.h, B, F, true))
+    if (!operand(&p.a[0], dy, B, dim, true) || !operand(&p.b[0], h, B, F, true) ||
+        !result(&p.out[0], dw_down, dim, F, add))
       return cudaErrorInvalidValue;
     e = add ? launch_gemm<kAdd32>(p, stream) : launch_gemm<kStore>(p, stream);
     if (e != cudaSuccess) return e;
