@@ -8,10 +8,10 @@
 // in, fp32 accumulation on the tcgen05 tensor cores.
 //
 // Every product runs through one kernel: clusters of two CTAs issue
-// tcgen05.mma.cta_group::2 of M = 256 rows (128 in each CTA) and N = 256
+// tcgen05.mma.cta_group::2 of M = 256 rows (128 in each CTA) and N = 256 or 128
 // columns, K in slabs of 64 through a ring of shared-memory stages filled by
-// TMA; 512 TMEM columns hold two accumulators, so a tile is multiplied while
-// the one before it is written out by eight epilogue warps.  Operands are
+// TMA; TMEM holds two accumulators, so a tile is multiplied while the one
+// before it is written out by eight epilogue warps.  Operands are
 // taken as they lie in memory: with K contiguous (K-major) or with M or N
 // contiguous (MN-major: the products with a transposed operand), both with
 // 128-byte swizzle.  What differs is the epilogue (Epi): each warp turns 32
@@ -20,8 +20,10 @@
 // touch 32 lines per instruction: the gate's epilogue took longer than its
 // product that way).
 //
-// Work is split evenly over the clusters (Plan): whole tiles while there is
-// one for every cluster, then what is left in equal stretches of K slabs.
+// One launch takes several products (the backward pass's last four), so that
+// small ones fill the GPU together.  Work is split evenly over the clusters
+// (Plan): whole tiles while there is one for every cluster, then, where that
+// pays, what is left in equal stretches of K slabs.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -38,53 +40,61 @@ namespace {
 using namespace tc;
 
 constexpr int FM = 128;                   // rows per CTA (the pair's MMA takes 2 * FM)
-constexpr int FN = 256;                   // accumulator columns per tile
 constexpr int FK = 64;                    // K per stage: one 128-byte swizzle row of bf16
 constexpr int FA_BYTES = FM * FK * 2;     // 16 KiB
-constexpr int FB_BYTES = FN / 2 * FK * 2; // 16 KiB: each CTA holds half of the columns
-constexpr int FSTAGE_BYTES = FA_BYTES + FB_BYTES;
-constexpr int FSTAGES = 5;
 constexpr int FEPI_WARPS = 8;
 constexpr int FOUT_BYTES = 8192;          // of an epilogue warp: four buffers of 32 x 32 bf16
-constexpr int FSMEM = FSTAGES * FSTAGE_BYTES + FEPI_WARPS * FOUT_BYTES + 1024;  // + alignment
 constexpr int FTHREADS = 64 + 32 * FEPI_WARPS;
-static_assert(FSMEM + 512 <= 227 * 1024, "feed-forward shared memory");
-
-enum Epi {
-  kGate,    // accumulator columns: 128 of g, the same 128 of u; writes h (and g, u)
-  kStore,   // C in bf16
-  kAdd32,   // C added to an fp32 matrix
-  kDGate    // accumulator: dh; reads g, u; writes dg, du, h
+// What goes with the tile's accumulator columns kN.
+template <int kN>
+struct Tile {
+  static constexpr int kB = kN / 2 * FK * 2;  // bytes of a B slab: each CTA holds half the columns
+  static constexpr int kStage = FA_BYTES + kB;
+  static constexpr int kStages = kN == 256 ? 5 : 6;
+  static constexpr int kSmem = kStages * kStage + FEPI_WARPS * FOUT_BYTES + 1024;  // + alignment
+  static_assert(kSmem + 512 <= 227 * 1024, "feed-forward shared memory");
 };
 
-// How a launch's tiles are split over its clusters.  With T tiles of kb slabs and C clusters,
-// the first T / C * C tiles are done whole, one per cluster and round.  The slabs of the R tiles
-// left are laid end to end and cut into C stretches of w: a stretch begins with the end of a tile
-// (its cluster writes those sums to memory: a part) and goes on with the beginning of the next,
-// whose cluster adds the other stretches' parts, waits for them if it must, and writes the tile.
-// Stretches are done first, and a cluster waits only for clusters of lower numbers, which start
-// before it and never wait before they have written their part.
+enum Epi {
+  kGate,   // accumulator columns: half of them g, the same half of u; writes h (and g, u)
+  kStore,  // C in bf16, or (Prod::add32) added to an fp32 matrix
+  kDGate   // accumulator: dh; reads g, u; writes dg, du, h
+};
+
+// How a launch's tiles are split over its clusters.  The products' tiles are numbered one product
+// after the other.  The first `whole` of them, one per cluster and round, are done whole.  The
+// slabs of those left, of kb slabs each, are laid end to end and cut into stretches of w: a
+// stretch begins with the end of a tile (its cluster writes those sums to memory: a part) and
+// goes on with the beginning of the next, whose cluster adds the other stretches' parts, waits
+// for them if it must, and writes the tile.  Stretches are done first, and a cluster waits only
+// for clusters of lower numbers, which start before it and never wait before they have written
+// their part.
 struct Plan {
   int tiles, kb, clusters;
   int whole;   // tiles done whole
   int w;       // slabs of a stretch, 0: no tile is cut (every tile is whole)
 };
 struct Seg {
-  int tile, k0, k1;
+  int tile, k0, k1;  // k1 < 0: all of the tile's slabs
   int part;    // >= 0: the sums go to this part instead of the tile
   int parts;   // of the tile, to be added: [first, first + parts)
   int first;
 };
 
-// One launch: `groups` products of one shape that differ in A and C (group i: a[i], b[i],
-// out[i]), or one product whose K runs through `segs` pairs (a[i], b[i]) one after the other.
+// A product: K runs through `segs` pairs (a[i], b[i]) one after the other.
+struct Prod {
+  CUtensorMap a[2], b[2], out;
+  int M, N, K;     // K of one segment
+  int segs;
+  int a_mn, b_mn;  // operand stored with M (N) contiguous
+  int add32;       // out is fp32 and added to
+  int tiles;
+};
+constexpr int kMaxProds = 4;
 struct GemmArgs {
-  CUtensorMap a[2], b[2];
-  CUtensorMap out[3];  // kGate: h, g, u; kStore, kAdd32: by group; kDGate: dg, du, h
-  int M, N, K;         // of one product; K of one segment
-  int segs, groups;    // at most one of them above 1
-  int a_mn, b_mn;      // operand stored with M (N) contiguous
-  int act, keep;       // keep: kGate writes g and u
+  Prod prod[kMaxProds];
+  CUtensorMap more[2];  // kGate (out: h): g, u; kDGate (out: dg): du, h
+  int prods, act, keep;  // keep: kGate writes g and u
   Plan plan;
   const __nv_bfloat16 *g_in, *u_in;  // kDGate
   float4* parts;                // [stretch][CTA of the pair][column / 4][row], part_rows rows
@@ -117,7 +127,7 @@ __device__ __forceinline__ bool seg_at(const Plan& p, int c, int i, Seg& s) {
     }
     i -= n;
   }
-  s.tile = c + i * p.clusters, s.k0 = 0, s.k1 = p.kb;
+  s.tile = c + i * p.clusters, s.k0 = 0, s.k1 = -1;
   return s.tile < p.whole;
 }
 
@@ -249,33 +259,35 @@ __device__ __forceinline__ void blocks_visible() {  // this thread's writes, to 
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Tile t of `groups` x (tm_count x tn_count): bands of 8 row tiles, within a
-// band row tiles fastest, so the tiles that run at one time share operands in L2.
-__device__ __forceinline__ void tile_at(int t, int tm_count, int tn_count, int& grp, int& tm,
-                                        int& tn) {
-  const int per = tm_count * tn_count;
-  grp = t / per;
-  t -= grp * per;
+// Tile t: its product, row tile and column tile (kTileN columns).  Within a product, bands of 8
+// row tiles, within a band row tiles fastest: tiles that run at one time share operands in L2.
+template <int kTileN>
+__device__ __forceinline__ const Prod& tile_at(const GemmArgs& p, int t, int& tm, int& tn) {
+  int i = 0;
+  while (i + 1 < p.prods && t >= p.prod[i].tiles) t -= p.prod[i++].tiles;
+  const Prod& q = p.prod[i];
+  const int tm_count = (q.M + 2 * FM - 1) / (2 * FM), tn_count = (q.N + kTileN - 1) / kTileN;
   const int band = t / (8 * tn_count);
   const int rows = min(8, tm_count - 8 * band);
   t -= band * 8 * tn_count;
   tn = t / rows;
   tm = band * 8 + t - tn * rows;
+  return q;
 }
 
-template <int kEpi>
+template <int kEpi, int kN>
 __global__ void __launch_bounds__(FTHREADS, 1)
 ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   extern __shared__ unsigned char smem_raw[];
+  constexpr int FSTAGES = Tile<kN>::kStages, FSTAGE_BYTES = Tile<kN>::kStage,
+                FB_BYTES = Tile<kN>::kB;
   __shared__ __align__(8) uint64_t bars[2 * FSTAGES + 4 + 1];
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
 
-  constexpr int kTileN = kEpi == kGate ? FN / 2 : FN;  // output columns per tile
-  const int tm_count = (p.M + 2 * FM - 1) / (2 * FM), tn_count = (p.N + kTileN - 1) / kTileN;
+  constexpr int kTileN = kEpi == kGate ? kN / 2 : kN;  // output columns per tile
   const uint32_t rank = cluster_ctarank();
   const int slot = (int)(blockIdx.x >> 1);
-  const int kb_seg = (p.K + FK - 1) / FK;
 
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -305,7 +317,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   if (warp == 1) {  // one warp of each CTA allocates, jointly for the pair
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&s_tmem_base)),
-                 "r"(512)
+                 "r"(2 * kN)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -323,12 +335,14 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       bool ok = true;
       Seg sg;
       for (int i = 0; ok && seg_at(p.plan, slot, i, sg); ++i) {
-        int grp, tm, tn;
-        tile_at(sg.tile, tm_count, tn_count, grp, tm, tn);
+        int tm, tn;
+        const Prod& q = tile_at<kTileN>(p, sg.tile, tm, tn);
         const int row0 = (2 * tm + (int)rank) * FM;
         // kGate: CTA 0 holds the tile's rows of Wg, CTA 1 those of Wu
-        const int col0 = kEpi == kGate ? tn * kTileN : tn * FN + (int)rank * (FN / 2);
-        for (int kb = sg.k0; kb < sg.k1; ++kb, ++it) {
+        const int col0 = kEpi == kGate ? tn * kTileN : tn * kN + (int)rank * (kN / 2);
+        const int kb_seg = (q.K + FK - 1) / FK, k1 = sg.k1 < 0 ? kb_seg * q.segs : sg.k1;
+        const bool a_mn = q.a_mn, b_mn = q.b_mn;
+        for (int kb = sg.k0; kb < k1; ++kb, ++it) {
           const uint32_t s = it % FSTAGES, ph = (it / FSTAGES) & 1u;
           if (!wait_phase_cluster(bar_empty(s), ph ^ 1u, ctl)) {
             ok = false;
@@ -336,19 +350,20 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
           }
           if (rank == 0) mbar_expect_tx(bar_full(s), 2u * FSTAGE_BYTES);
           const int seg = kb / kb_seg, k0 = (kb - seg * kb_seg) * FK;
-          const CUtensorMap* ma = &p.a[seg + grp];
-          const CUtensorMap* mb = kEpi == kGate ? &p.b[rank] : &p.b[seg + grp];
+          const CUtensorMap* ma = &q.a[seg];
+          const CUtensorMap* mb = kEpi == kGate ? &q.b[rank] : &q.b[seg];
           const uint32_t da = stages_u32 + s * FSTAGE_BYTES, db = da + FA_BYTES;
           const uint32_t fb = mapa_shared(bar_full(s), 0);
-          if (p.a_mn) {
+          if (a_mn) {
             tma_load_2d_cg2(da, ma, row0, k0, fb);
             tma_load_2d_cg2(da + FA_BYTES / 2, ma, row0 + 64, k0, fb);
           } else {
             tma_load_2d_cg2(da, ma, k0, row0, fb);
           }
-          if (p.b_mn) {
-            tma_load_2d_cg2(db, mb, col0, k0, fb);
-            tma_load_2d_cg2(db + FB_BYTES / 2, mb, col0 + 64, k0, fb);
+          if (b_mn) {
+#pragma unroll
+            for (int j = 0; j < kN / 128; ++j)
+              tma_load_2d_cg2(db + j * 64 * FK * 2, mb, col0 + 64 * j, k0, fb);
           } else {
             tma_load_2d_cg2(db, mb, k0, col0, fb);
           }
@@ -364,11 +379,6 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader)
     if (rank == 0 && lane == 0) {
-      const uint32_t idesc = idesc_bf16(2 * FM, FN) | (p.a_mn ? kIdescAMn : 0u) |
-                             (p.b_mn ? kIdescBMn : 0u);
-      // descriptor advance per 16 of K: 32 bytes along a swizzled row, or 16
-      // rows of 128 bytes
-      const uint32_t a_step = p.a_mn ? 128u : 2u, b_step = p.b_mn ? 128u : 2u;
       uint32_t it = 0;
       bool ok = true;
       Seg sg;
@@ -376,7 +386,15 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
         const uint32_t buf = i & 1u, use = i >> 1;
         if (!wait_phase_cluster(bar_tempty(buf), (use & 1u) ^ 1u, ctl)) break;
         tc_fence_after();
-        for (int kb = sg.k0; kb < sg.k1; ++kb, ++it) {
+        int tm, tn;
+        const Prod& q = tile_at<kTileN>(p, sg.tile, tm, tn);
+        const bool a_mn = q.a_mn, b_mn = q.b_mn;
+        const uint32_t idesc =
+            idesc_bf16(2 * FM, kN) | (a_mn ? kIdescAMn : 0u) | (b_mn ? kIdescBMn : 0u);
+        // descriptor advance per 16 of K: 32 bytes along a swizzled row, or 16 rows of 128 bytes
+        const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
+        const int k1 = sg.k1 < 0 ? (q.K + FK - 1) / FK * q.segs : sg.k1;
+        for (int kb = sg.k0; kb < k1; ++kb, ++it) {
           const uint32_t s = it % FSTAGES, ph = (it / FSTAGES) & 1u;
           if (!wait_phase_cluster(bar_full(s), ph, ctl)) {
             ok = false;
@@ -384,12 +402,12 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
           }
           tc_fence_after();
           const uint32_t sa = stages_u32 + s * FSTAGE_BYTES;
-          const uint64_t a_desc = p.a_mn ? sw128_mn_desc(sa, FA_BYTES / 2) : sw128_desc(sa);
-          const uint64_t b_desc = p.b_mn ? sw128_mn_desc(sa + FA_BYTES, FB_BYTES / 2)
-                                         : sw128_desc(sa + FA_BYTES);
+          const uint64_t a_desc = a_mn ? sw128_mn_desc(sa, 64 * FK * 2) : sw128_desc(sa);
+          const uint64_t b_desc = b_mn ? sw128_mn_desc(sa + FA_BYTES, 64 * FK * 2)
+                                       : sw128_desc(sa + FA_BYTES);
 #pragma unroll
           for (int kk = 0; kk < FK / 16; ++kk)
-            tc_mma_cg2(tmem + buf * FN, a_desc + a_step * kk, b_desc + b_step * kk, idesc,
+            tc_mma_cg2(tmem + buf * kN, a_desc + a_step * kk, b_desc + b_step * kk, idesc,
                        kb != sg.k0 || kk != 0);
           tc_commit_cg2_mc(bar_empty(s), 3);  // the stage is free again in both CTAs
         }
@@ -405,23 +423,24 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
     const int quad = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t bufs = stages_u32 + FSTAGES * FSTAGE_BYTES + ew * FOUT_BYTES;
-    uint32_t nb = 0;  // next buffer (of four; of two for fp32 blocks)
+    uint32_t nb = 0;  // next buffer of four
     Seg sg;
     for (int i = 0; seg_at(p.plan, slot, i, sg); ++i) {
-      int grp, tm, tn;
-      tile_at(sg.tile, tm_count, tn_count, grp, tm, tn);
+      int tm, tn;
+      const Prod& q = tile_at<kTileN>(p, sg.tile, tm, tn);
+      const int M = q.M, N = q.N;
       const uint32_t buf = i & 1u, use = i >> 1;
-      const uint32_t taddr = lane_addr + buf * FN;
+      const uint32_t taddr = lane_addr + buf * kN;
       const int row0 = (2 * tm + (int)rank) * FM + quad * 32;  // of the warp
       const int row = row0 + lane;
       constexpr int kHalfN = kTileN / 2;
-      const int cols = min(kHalfN, p.N - tn * kTileN - half * kHalfN);  // may be <= 0
+      const int cols = min(kHalfN, N - tn * kTileN - half * kHalfN);  // may be <= 0
       const int col0 = tn * kTileN + half * kHalfN;
-      const bool in = row < p.M;
+      const bool in = row < M;
       // this thread's part of a stretch's sums: [column / 4][row]
       const int prow = quad * 32 + lane;
       auto part_at = [&](int r) {
-        return p.parts + ((size_t)(2 * r + rank) * (FN / 4)) * p.part_rows + prow;
+        return p.parts + ((size_t)(2 * r + rank) * (kN / 4)) * p.part_rows + prow;
       };
       auto flag_at = [&](int r) { return p.flags + (size_t)(2 * r + rank) * FEPI_WARPS + ew; };
 
@@ -433,8 +452,8 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
           for (int j = 0; j < 4; ++j) {
             const int r = row0 + 8 * j + (lane >> 2), cc = c + 8 * (lane & 3);
             pg[j] = pu[j] = make_uint4(0, 0, 0, 0);
-            if (r < p.M && cc < cols) {
-              const size_t at = (size_t)r * p.N + col0 + cc;
+            if (r < M && cc < cols) {
+              const size_t at = (size_t)r * N + col0 + cc;
               pg[j] = __ldcs(reinterpret_cast<const uint4*>(p.g_in + at));
               pu[j] = __ldcs(reinterpret_cast<const uint4*>(p.u_in + at));
             }
@@ -444,7 +463,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       if (kEpi == kDGate && sg.part < 0) {
         if (in)  // the rest of the tile into L2 meanwhile (128 bytes at a time)
           for (int c = 64; c < cols; c += 64) {
-            const size_t at = (size_t)row * p.N + col0 + c;
+            const size_t at = (size_t)row * N + col0 + c;
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.g_in + at));
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.u_in + at));
           }
@@ -452,13 +471,13 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       }
       if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_tfull(buf), use & 1u, ctl))) break;
       tc_fence_after();
-      if (row0 < p.M && cols > 0) {
+      if (row0 < M && cols > 0) {
         if (sg.part >= 0) {
           float4* dst = part_at(sg.part);
           for (int c = 0; c < cols; c += 32) {
 #pragma unroll
             for (int q = 0; q < (kEpi == kGate ? 2 : 1); ++q) {
-              const int tc = half * kHalfN + c + q * (FN / 2);
+              const int tc = half * kHalfN + c + q * (kN / 2);
               float v[32];
               tmem_ld32(taddr + tc, v);
               if (in)
@@ -515,7 +534,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
             if constexpr (kEpi == kGate) {
               float w[32];
               sums(tc, v);
-              sums(FN / 2 + tc, w);
+              sums(kN / 2 + tc, w);
               if (lane == 0) blocks_read<1>();
               __syncwarp();
               const uint32_t b0 = next_buf();
@@ -533,35 +552,38 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               blocks_visible();
               __syncwarp();
               if (lane == 0) {
-                store_block(&p.out[0], b0, gc, row0);
+                store_block(&q.out, b0, gc, row0);
                 if (p.keep) {
-                  store_block(&p.out[1], b1, gc, row0);
-                  store_block(&p.out[2], b2, gc, row0);
+                  store_block(&p.more[0], b1, gc, row0);
+                  store_block(&p.more[1], b2, gc, row0);
                 }
               }
             } else if constexpr (kEpi == kStore) {
               sums(tc, v);
-              if (lane == 0) blocks_read<3>();
-              __syncwarp();
-              const uint32_t b0 = next_buf();
-              put_row(b0, lane, v);
-              blocks_visible();
-              __syncwarp();
-              if (lane == 0) store_block(&p.out[grp], b0, gc, row0);
-            } else if constexpr (kEpi == kAdd32) {
-              sums(tc, v);
-              if (lane == 0) blocks_read<1>();
-              __syncwarp();
-              const uint32_t b0 = bufs + (nb & 1) * 4096;
-              ++nb;
+              if (!q.add32) {
+                if (lane == 0) blocks_read<1>();  // (the last may be an fp32 block, two buffers)
+                __syncwarp();
+                const uint32_t b0 = next_buf();
+                put_row(b0, lane, v);
+                blocks_visible();
+                __syncwarp();
+                if (lane == 0) store_block(&q.out, b0, gc, row0);
+              } else {
+                // two buffers of twice the size (the blocks of a product before this one that
+                // still lie in them are read first)
+                if (lane == 0) blocks_read<0>();
+                __syncwarp();
+                const uint32_t b0 = bufs + (nb & 2) * 2048;
+                nb = (nb + 2) & 3;
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                sts(at128(b0, lane, j),
-                    make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                               __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
-              blocks_visible();
-              __syncwarp();
-              if (lane == 0) add_block(&p.out[grp], b0, gc, row0);
+                for (int j = 0; j < 8; ++j)
+                  sts(at128(b0, lane, j),
+                      make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                 __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+                blocks_visible();
+                __syncwarp();
+                if (lane == 0) add_block(&q.out, b0, gc, row0);
+              }
             } else {
               if (lane == 0) blocks_read<1>();
               __syncwarp();
@@ -592,9 +614,9 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               blocks_visible();
               __syncwarp();
               if (lane == 0) {
-                store_block(&p.out[0], b0, gc, row0);
-                store_block(&p.out[1], b1, gc, row0);
-                store_block(&p.out[2], b2, gc, row0);
+                store_block(&q.out, b0, gc, row0);
+                store_block(&p.more[0], b1, gc, row0);
+                store_block(&p.more[1], b2, gc, row0);
               }
             }
           }
@@ -615,7 +637,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kN)
                  : "memory");
   }
 }
@@ -632,9 +654,10 @@ bool encode2(CUtensorMap* m, const void* ptr, int rows, int cols, int box_cols, 
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// An operand whose rows are M (N) and whose columns are K, or the transpose.
-bool operand(CUtensorMap* m, const void* ptr, int rows, int cols, bool mn) {
-  return encode2(m, ptr, rows, cols, 64, mn ? FK : FM);
+// An operand whose rows are M (N) and whose columns are K, or the transpose; `rows` of it (64 for
+// the transpose) are one CTA's in a slab.
+bool operand(CUtensorMap* m, const void* ptr, int rows, int cols, bool mn, int box = FM) {
+  return encode2(m, ptr, rows, cols, 64, mn ? FK : box);
 }
 // A result [rows, cols] in blocks of 32 x 32, bf16 or fp32.
 bool result(CUtensorMap* m, void* ptr, int rows, int cols, bool f32 = false) {
@@ -652,12 +675,12 @@ bool result(CUtensorMap* m, void* ptr, int rows, int cols, bool f32 = false) {
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Parts of cut tiles, of products with at most M rows: [cluster][2][FN / 4][rows] float4, and
+// Parts of cut tiles, of products with at most M rows: [cluster][2][columns / 4][rows] float4, and
 // their flags.
-constexpr int kMaxClusters = 80;
+constexpr int kMaxClusters = 80, kMaxN = 256;
 int part_rows(int M) { return M >= FM ? FM : (M + 31) / 32 * 32; }
 size_t parts_bytes(int M) {
-  return align256((size_t)kMaxClusters * 2 * FN * part_rows(M) * 4) +
+  return align256((size_t)kMaxClusters * 2 * kMaxN * part_rows(M) * 4) +
          align256((size_t)kMaxClusters * 2 * FEPI_WARPS * 8);
 }
 void set_parts(GemmArgs& p, void* ws, int M) {
@@ -665,7 +688,7 @@ void set_parts(GemmArgs& p, void* ws, int M) {
   p.parts = static_cast<float4*>(ws);
   p.flags = reinterpret_cast<unsigned long long*>(
       static_cast<unsigned char*>(ws) +
-      align256((size_t)kMaxClusters * 2 * FN * p.part_rows * 4));
+      align256((size_t)kMaxClusters * 2 * kMaxN * p.part_rows * 4));
 }
 
 // The value of this launch's flags.  The workspace is whatever its memory held before: a flag
@@ -679,9 +702,57 @@ unsigned long long next_epoch() {
   return e ? e : n.fetch_add(1, std::memory_order_relaxed);
 }
 
-template <int kEpi>
-cudaError_t launch_gemm(GemmArgs& p, cudaStream_t stream) {
-  auto kernel = ffn_gemm_kernel<kEpi>;
+// The products of p in tiles of kN columns over at most `most` clusters, and how long that takes,
+// in slabs of a 256-column tile.
+Plan plan_of(const GemmArgs& p, int epi, int kN, int most, double* cost) {
+  const int tile_n = epi == kGate ? kN / 2 : kN;
+  Plan pl = {};
+  int64_t slabs = 0;
+  int rows = 0, longest = 0;
+  for (int i = 0; i < p.prods; ++i) {
+    const Prod& q = p.prod[i];
+    const int t = (q.M + 2 * FM - 1) / (2 * FM) * ((q.N + tile_n - 1) / tile_n);
+    const int kb = (q.K + FK - 1) / FK * q.segs;
+    pl.tiles += t;
+    slabs += (int64_t)t * kb;
+    rows = q.M > rows ? q.M : rows;
+    longest = kb > longest ? kb : longest;
+    pl.kb = kb;
+  }
+  if (rows > 2 * FM) rows = 2 * FM;
+  // a slab of 128 columns takes about 0.6 of one of 256 (both operands' bytes: 24 of 32 KB)
+  const double slab = kN == 256 ? 1.0 : 0.6;
+  pl.clusters = pl.tiles < most ? pl.tiles : most;
+  pl.whole = pl.tiles;
+  double rounds;  // of the longest tile
+  const int left = pl.tiles % most;
+  if (p.prods == 1)
+    rounds = (double)((pl.tiles + most - 1) / most) * pl.kb;
+  else  // tiles of several lengths even out
+    rounds = (double)slabs / most + 0.5 * longest > longest ? (double)slabs / most + 0.5 * longest
+                                                             : longest;
+  // Cutting (one product): a tile into up to 4.  A part costs about 10 slabs' time to write, to
+  // wait for and to read, for all 256 rows and columns, each further one 3.
+  if (p.prods == 1 && left) {
+    int64_t w = ((int64_t)left * pl.kb + most - 1) / most;
+    if (w < (pl.kb + 3) / 4) w = (pl.kb + 3) / 4;
+    const int parts = (int)((pl.kb + w - 1) / w);  // and one more where stretches straddle tiles
+    const double area = (rows / (2.0 * FM)) * (kN / 256.0);
+    const double extra = 4 + (6 + 3 * parts) * area;
+    if (w * slab + extra < pl.kb * slab && (int64_t)left * pl.kb < INT32_MAX / 2) {
+      pl.w = (int)w;
+      pl.whole = pl.tiles - left;
+      rounds -= pl.kb - w - extra / slab;
+      pl.clusters = pl.whole ? most : (int)(((int64_t)left * pl.kb + w - 1) / w);
+    }
+  }
+  *cost = rounds * slab;
+  return pl;
+}
+
+template <int kEpi, int kN>
+cudaError_t launch_tiles(GemmArgs& p, cudaStream_t stream, int* most) {
+  auto kernel = ffn_gemm_kernel<kEpi, kN>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -689,49 +760,58 @@ cudaError_t launch_gemm(GemmArgs& p, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(FTHREADS);
-  cfg.dynamicSmemBytes = FSMEM;
+  cfg.dynamicSmemBytes = Tile<kN>::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  static int max_clusters = 0;
-  if (!max_clusters) {
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FSMEM);
+  if (most) {  // how many clusters run at one time
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Tile<kN>::kSmem);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(2 * (sm_count() / 2));
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
-    max_clusters = n < kMaxClusters ? n : kMaxClusters;
+    *most = n < kMaxClusters ? n : kMaxClusters;
+    return cudaSuccess;
   }
-  const int tile_n = kEpi == kGate ? FN / 2 : FN;
-  Plan& pl = p.plan;
-  pl.tiles = (p.M + 2 * FM - 1) / (2 * FM) * ((p.N + tile_n - 1) / tile_n) * p.groups;
-  pl.kb = (p.K + FK - 1) / FK * p.segs;
-  pl.clusters = max_clusters;
-  pl.whole = pl.tiles / max_clusters * max_clusters;
-  const int left = pl.tiles - pl.whole;
-  pl.w = 0;
-  if (left) {
-    // Cutting pays when a stretch is shorter than a tile by more than its part costs to write
-    // and to read back, in slabs: about 3, and 8 more for all rows of a tile.
-    const int64_t slabs = (int64_t)left * pl.kb;
-    const int cost = 3 + 8 * (p.M < 2 * FM ? p.M : 2 * FM) / (2 * FM);
-    int64_t w = (slabs + max_clusters - 1) / max_clusters;
-    if (w < 2) w = 2;  // (fewer clusters, but each with something in flight)
-    if (w + cost < pl.kb && slabs < INT32_MAX / 2)
-      pl.w = (int)w;
-    else
-      pl.whole = pl.tiles;
-  }
-  if (pl.w && !pl.whole)  // fewer stretches than clusters
-    pl.clusters = (int)(((int64_t)left * pl.kb + pl.w - 1) / pl.w);
-  else if (!pl.w && pl.tiles < max_clusters)
-    pl.clusters = pl.tiles;
-  p.epoch = next_epoch();
-  cfg.gridDim = dim3(2 * (unsigned)pl.clusters);
+  cfg.gridDim = dim3(2 * (unsigned)p.plan.clusters);
   return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// B operands are encoded here, for the tile's width.
+struct BOperand {
+  const void* ptr;
+  int rows, cols;
+};
+template <int kEpi>
+cudaError_t launch_gemm(GemmArgs& p, const BOperand (&b)[kMaxProds][2], cudaStream_t stream) {
+  static int most[2];
+  if (!most[0]) {
+    cudaError_t e = launch_tiles<kEpi, 256>(p, stream, &most[0]);
+    if (e != cudaSuccess) return e;
+  }
+  if (!most[1]) {
+    cudaError_t e = launch_tiles<kEpi, 128>(p, stream, &most[1]);
+    if (e != cudaSuccess) return e;
+  }
+  double c256, c128;
+  const Plan p256 = plan_of(p, kEpi, 256, most[0], &c256);
+  const Plan p128 = plan_of(p, kEpi, 128, most[1], &c128);
+  const bool wide = c256 <= c128;
+  p.plan = wide ? p256 : p128;
+  const int kN = wide ? 256 : 128, tile_n = kEpi == kGate ? kN / 2 : kN;
+  for (int i = 0; i < p.prods; ++i) {
+    Prod& q = p.prod[i];
+    q.tiles = (q.M + 2 * FM - 1) / (2 * FM) * ((q.N + tile_n - 1) / tile_n);
+    for (int j = 0; j < (kEpi == kGate ? 2 : q.segs); ++j)
+      if (!operand(&q.b[j], b[i][j].ptr, b[i][j].rows, b[i][j].cols, q.b_mn, kN / 2))
+        return cudaErrorInvalidValue;
+  }
+  p.epoch = next_epoch();
+  return wide ? launch_tiles<kEpi, 256>(p, stream, nullptr)
+              : launch_tiles<kEpi, 128>(p, stream, nullptr);
 }
 
 }  // namespace
@@ -747,23 +827,23 @@ cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up
                              const void* w_down, int B, int dim, int F, int act, void* workspace,
                              void* y, void* gate, void* up, int* status, cudaStream_t stream) {
   GemmArgs p = {};
-  p.segs = p.groups = 1;
+  p.prods = 1;
   p.act = act;
   p.status = status;
-  p.M = B, p.N = F, p.K = dim;
   p.keep = gate != nullptr;
   set_parts(p, static_cast<unsigned char*>(workspace) + align256((size_t)B * F * 2), B);
-  if (!operand(&p.a[0], x, B, dim, false) || !operand(&p.b[0], w_gate, F, dim, false) ||
-      !operand(&p.b[1], w_up, F, dim, false) || !result(&p.out[0], workspace, B, F) ||
-      (gate && (!result(&p.out[1], gate, B, F) || !result(&p.out[2], up, B, F))))
+  Prod& q = p.prod[0];
+  q.segs = 1;
+  q.M = B, q.N = F, q.K = dim;
+  if (!operand(&q.a[0], x, B, dim, false) || !result(&q.out, workspace, B, F) ||
+      (gate && (!result(&p.more[0], gate, B, F) || !result(&p.more[1], up, B, F))))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_gemm<kGate>(p, stream);
+  cudaError_t e = launch_gemm<kGate>(p, {{{w_gate, F, dim}, {w_up, F, dim}}}, stream);
   if (e != cudaSuccess) return e;
-  p.N = dim, p.K = F;
-  if (!operand(&p.a[0], workspace, B, F, false) || !operand(&p.b[0], w_down, dim, F, false) ||
-      !result(&p.out[0], y, B, dim))
+  q.N = dim, q.K = F;
+  if (!operand(&q.a[0], workspace, B, F, false) || !result(&q.out, y, B, dim))
     return cudaErrorInvalidValue;
-  return launch_gemm<kStore>(p, stream);
+  return launch_gemm<kStore>(p, {{{w_down, dim, F}}}, stream);
 }
 
 cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const void* w_up,
@@ -776,50 +856,52 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
   const size_t part = align256((size_t)B * F * 2);
   void *dg = ws, *du = ws + part, *h = ws + 2 * part;
   GemmArgs p = {};
-  p.segs = p.groups = 1;
+  p.prods = 1;
   p.act = act;
   p.status = status;
   p.g_in = static_cast<const __nv_bfloat16*>(gate);
   p.u_in = static_cast<const __nv_bfloat16*>(up);
   set_parts(p, ws + 3 * part, FM);
-  // dh = dy Wd, then dg, du and h
-  p.M = B, p.N = F, p.K = dim, p.b_mn = 1;
-  if (!operand(&p.a[0], dy, B, dim, false) || !operand(&p.b[0], w_down, dim, F, true) ||
-      !result(&p.out[0], dg, B, F) || !result(&p.out[1], du, B, F) || !result(&p.out[2], h, B, F))
-    return cudaErrorInvalidValue;
-  cudaError_t e = launch_gemm<kDGate>(p, stream);
-  if (e != cudaSuccess) return e;
-  if (dx) {  // dx = dg Wg + du Wu: one product of twice the depth
-    p.N = dim, p.K = F, p.segs = 2;
-    if (!operand(&p.a[0], dg, B, F, false) || !operand(&p.a[1], du, B, F, false) ||
-        !operand(&p.b[0], w_gate, F, dim, true) || !operand(&p.b[1], w_up, F, dim, true) ||
-        !result(&p.out[0], dx, B, dim))
+  {  // dh = dy Wd, then dg, du and h
+    Prod& q = p.prod[0];
+    q.segs = 1;
+    q.M = B, q.N = F, q.K = dim, q.b_mn = 1;
+    if (!operand(&q.a[0], dy, B, dim, false) || !result(&q.out, dg, B, F) ||
+        !result(&p.more[0], du, B, F) || !result(&p.more[1], h, B, F))
       return cudaErrorInvalidValue;
-    if ((e = launch_gemm<kStore>(p, stream)) != cudaSuccess) return e;
-    p.segs = 1;
+    cudaError_t e = launch_gemm<kDGate>(p, {{{w_down, dim, F}}}, stream);
+    if (e != cudaSuccess) return e;
   }
+  // the rest in one launch
   const bool add = grad_dtype == PKM_F32;
-  p.a_mn = 1, p.K = B;
-  if (dw_gate) {  // dWg = dg^T x and dWu = du^T x
-    p.M = F, p.N = dim, p.groups = 2;
-    if (!operand(&p.a[0], dg, B, F, true) || !operand(&p.a[1], du, B, F, true) ||
-        !operand(&p.b[0], x, B, dim, true) || !result(&p.out[0], dw_gate, F, dim, add) ||
-        !result(&p.out[1], dw_up, F, dim, add))
-      return cudaErrorInvalidValue;
-    p.b[1] = p.b[0];
-    e = add ? launch_gemm<kAdd32>(p, stream) : launch_gemm<kStore>(p, stream);
-    if (e != cudaSuccess) return e;
-    p.groups = 1;
-  }
-  if (dw_down) {  // dWd = dy^T h
-    p.M = dim, p.N = F;
-    if (!operand(&p.a[0], dy, B, dim, true) || !operand(&p.b[0], h, B, F, true) ||
-        !result(&p.out[0], dw_down, dim, F, add))
-      return cudaErrorInvalidValue;
-    e = add ? launch_gemm<kAdd32>(p, stream) : launch_gemm<kStore>(p, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  BOperand b[kMaxProds][2] = {};
+  p.prods = 0;
+  auto weight = [&](const void* a, int rows, const void* bp, int cols, void* out) {
+    Prod& q = p.prod[p.prods];  // out [rows, cols] = a^T b over the batch
+    q = Prod{};
+    q.segs = 1;
+    q.M = rows, q.N = cols, q.K = B, q.a_mn = q.b_mn = 1, q.add32 = add;
+    b[p.prods++][0] = {bp, B, cols};
+    return operand(&q.a[0], a, B, rows, true) && result(&q.out, out, rows, cols, add);
+  };
+  auto input = [&] {  // dx = dg Wg + du Wu: one product of twice the depth
+    Prod& q = p.prod[p.prods];
+    q = Prod{};
+    q.segs = 2;
+    q.M = B, q.N = dim, q.K = F, q.b_mn = 1;
+    b[p.prods][0] = {w_gate, F, dim};
+    b[p.prods++][1] = {w_up, F, dim};
+    return operand(&q.a[0], dg, B, F, false) && operand(&q.a[1], du, B, F, false) &&
+           result(&q.out, dx, B, dim);
+  };
+  // longest tiles first: shorter ones fill the last rounds
+  const bool first = 2 * (int64_t)F >= B;
+  if (dx && first && !input()) return cudaErrorInvalidValue;
+  if (dw_gate && (!weight(dg, F, x, dim, dw_gate) || !weight(du, F, x, dim, dw_up)))
+    return cudaErrorInvalidValue;
+  if (dw_down && !weight(dy, dim, h, F, dw_down)) return cudaErrorInvalidValue;
+  if (dx && !first && !input()) return cudaErrorInvalidValue;
+  return p.prods ? launch_gemm<kStore>(p, b, stream) : cudaSuccess;
 }
 
 }  // namespace pkm
@@ -846,8 +928,8 @@ int ffn_check(int B, int dim, int F, int act) {
   // the kernels count tiles (of 128 x 128 at the smallest) and rows in 32 bits
   constexpr int most = INT32_MAX - 256;
   auto t = [](int n) { return ((int64_t)n + 127) / 128; };
-  if (B > most || dim > most || F > most || t(B) * t(F) > most || t(B) * t(dim) > most ||
-      2 * t(F) * t(dim) > most)
+  if (B > most || dim > most || F > most || t(B) * t(F) > most / 4 || t(B) * t(dim) > most / 4 ||
+      t(F) * t(dim) > most / 4)
     return PKM_ERR_RANGE;
   return PKM_OK;
 }
