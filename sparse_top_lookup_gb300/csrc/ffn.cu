@@ -292,7 +292,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t stages_u32 = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t bar0 = smem_u32(&bars[0]);
   auto bar_full = [&](uint32_t s) { return bar0 + 8u * s; };
   auto bar_empty = [&](uint32_t s) { return bar0 + 8u * (FSTAGES + s); };
@@ -328,32 +328,35 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   const uint32_t tmem = s_tmem_base;
   const Ctl ctl{&s_abort, p.status};
 
+  // The two issuing warps run their loops with all lanes and elect one only around what it
+  // issues: with the loop in one lane's branch a step took 0.22 us more or less whatever it
+  // copied, as long as a slab's MMAs; so it takes 0.13.
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      Seg sg;
-      for (int i = 0; ok && seg_at(p.plan, slot, i, sg); ++i) {
-        int tm, tn;
-        const Prod& q = tile_at<kTileN>(p, sg.tile, tm, tn);
-        const int row0 = (2 * tm + (int)rank) * FM;
-        // kGate: CTA 0 holds the tile's rows of Wg, CTA 1 those of Wu
-        const int col0 = kEpi == kGate ? tn * kTileN : tn * kN + (int)rank * (kN / 2);
-        const int kb_seg = (q.K + FK - 1) / FK, k1 = sg.k1 < 0 ? kb_seg * q.segs : sg.k1;
-        const bool a_mn = q.a_mn, b_mn = q.b_mn;
-        for (int kb = sg.k0; kb < k1; ++kb, ++it) {
-          const uint32_t s = it % FSTAGES, ph = (it / FSTAGES) & 1u;
-          if (!wait_phase_cluster(bar_empty(s), ph ^ 1u, ctl)) {
-            ok = false;
-            break;
-          }
+    uint32_t s = 0, ph = 1, used = 0;
+    const uint32_t full0 = mapa_shared(bar0, 0);  // the leader's barriers
+    bool ok = true;
+    Seg sg;
+    for (int i = 0; ok && seg_at(p.plan, slot, i, sg); ++i) {
+      int tm, tn;
+      const Prod& q = tile_at<kTileN>(p, sg.tile, tm, tn);
+      const int row0 = (2 * tm + (int)rank) * FM;
+      // kGate: CTA 0 holds the tile's rows of Wg, CTA 1 those of Wu
+      const int col0 = kEpi == kGate ? tn * kTileN : tn * kN + (int)rank * (kN / 2);
+      const int kb_seg = (q.K + FK - 1) / FK, k1 = sg.k1 < 0 ? kb_seg * q.segs : sg.k1;
+      const bool a_mn = q.a_mn, b_mn = q.b_mn;
+      int seg = sg.k0 / kb_seg, k0 = (sg.k0 - seg * kb_seg) * FK;
+      for (int kb = sg.k0; kb < k1; ++kb) {
+        if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_empty(s), ph, ctl))) {
+          ok = false;
+          break;
+        }
+        const uint32_t da = stages_u32 + s * FSTAGE_BYTES, db = da + FA_BYTES;
+        const uint32_t fb = full0 + 8u * s;
+        const CUtensorMap* ma = &q.a[seg];
+        const CUtensorMap* mb = kEpi == kGate ? &q.b[rank] : &q.b[seg];
+        if (elect_one()) {
           if (rank == 0) mbar_expect_tx(bar_full(s), 2u * FSTAGE_BYTES);
-          const int seg = kb / kb_seg, k0 = (kb - seg * kb_seg) * FK;
-          const CUtensorMap* ma = &q.a[seg];
-          const CUtensorMap* mb = kEpi == kGate ? &q.b[rank] : &q.b[seg];
-          const uint32_t da = stages_u32 + s * FSTAGE_BYTES, db = da + FA_BYTES;
-          const uint32_t fb = mapa_shared(bar_full(s), 0);
           if (a_mn) {
             tma_load_2d_cg2(da, ma, row0, k0, fb);
             tma_load_2d_cg2(da + FA_BYTES / 2, ma, row0 + 64, k0, fb);
@@ -368,23 +371,30 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
             tma_load_2d_cg2(db, mb, k0, col0, fb);
           }
         }
-      }
-      // the leader's last releases of this CTA's stages land before it exits
-      if (ok) {
-        const uint32_t first = it > (uint32_t)FSTAGES ? it - FSTAGES : 0u;
-        for (uint32_t j = first; j < it; ++j)
-          wait_phase_drain(bar_empty(j % FSTAGES), (j / FSTAGES) & 1u);
+        __syncwarp();
+        if (used < (uint32_t)FSTAGES) ++used;
+        if (++s == (uint32_t)FSTAGES) s = 0, ph ^= 1u;
+        k0 += FK;
+        if (k0 >= q.K) k0 = 0, ++seg;
       }
     }
+    // the leader's last releases of this CTA's stages land before it exits
+    if (ok)
+      for (uint32_t j = 0; j < used; ++j) {
+        if (s == 0) s = FSTAGES, ph ^= 1u;
+        --s;
+        wait_phase_drain(bar_empty(s), ph ^ 1u);
+      }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader)
-    if (rank == 0 && lane == 0) {
-      uint32_t it = 0;
+    if (rank == 0) {
+      uint32_t s = 0, ph = 0;
       bool ok = true;
       Seg sg;
       for (int i = 0; ok && seg_at(p.plan, slot, i, sg); ++i) {
         const uint32_t buf = i & 1u, use = i >> 1;
-        if (!wait_phase_cluster(bar_tempty(buf), (use & 1u) ^ 1u, ctl)) break;
+        if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_tempty(buf), (use & 1u) ^ 1u, ctl)))
+          break;
         tc_fence_after();
         int tm, tn;
         const Prod& q = tile_at<kTileN>(p, sg.tile, tm, tn);
@@ -394,9 +404,8 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
         // descriptor advance per 16 of K: 32 bytes along a swizzled row, or 16 rows of 128 bytes
         const uint32_t a_step = a_mn ? 128u : 2u, b_step = b_mn ? 128u : 2u;
         const int k1 = sg.k1 < 0 ? (q.K + FK - 1) / FK * q.segs : sg.k1;
-        for (int kb = sg.k0; kb < k1; ++kb, ++it) {
-          const uint32_t s = it % FSTAGES, ph = (it / FSTAGES) & 1u;
-          if (!wait_phase_cluster(bar_full(s), ph, ctl)) {
+        for (int kb = sg.k0; kb < k1; ++kb) {
+          if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_full(s), ph, ctl))) {
             ok = false;
             break;
           }
@@ -405,17 +414,22 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
           const uint64_t a_desc = a_mn ? sw128_mn_desc(sa, 64 * FK * 2) : sw128_desc(sa);
           const uint64_t b_desc = b_mn ? sw128_mn_desc(sa + FA_BYTES, 64 * FK * 2)
                                        : sw128_desc(sa + FA_BYTES);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < FK / 16; ++kk)
-            tc_mma_cg2(tmem + buf * kN, a_desc + a_step * kk, b_desc + b_step * kk, idesc,
-                       kb != sg.k0 || kk != 0);
-          tc_commit_cg2_mc(bar_empty(s), 3);  // the stage is free again in both CTAs
+            for (int kk = 0; kk < FK / 16; ++kk)
+              tc_mma_cg2(tmem + buf * kN, a_desc + a_step * kk, b_desc + b_step * kk, idesc,
+                         kb != sg.k0 || kk != 0);
+            tc_commit_cg2_mc(bar_empty(s), 3);  // the stage is free again in both CTAs
+            // the tile's sums are in both TMEMs
+            if (kb + 1 == k1) tc_commit_cg2_mc(bar_tfull(buf), 3);
+          }
+          __syncwarp();
+          if (++s == (uint32_t)FSTAGES) s = 0, ph ^= 1u;
         }
-        if (!ok) break;
-        tc_commit_cg2_mc(bar_tfull(buf), 3);  // the tile's sums are in both TMEMs
       }
       // every issued MMA completes before TMEM is released
-      tc_commit_cg2_mc(bar_done, 1);
+      if (elect_one()) tc_commit_cg2_mc(bar_done, 1);
+      __syncwarp();
       wait_phase_drain(bar_done, 0);
     }
   } else {

@@ -223,6 +223,17 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+// One lane of a converged warp (the same one each time while the warp stays converged).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Every thread of every CTA of the cluster (release / acquire).
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -325,12 +336,17 @@ struct Ctl {
   int* status;
 };
 
+// Polls between two looks at the clock: a wait that has to poll mostly ends without one.
+constexpr int kPolls = 64;
+
 // Waits for the phase of the given parity; false on time-out or abort.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Ctl& ctl) {
-  if (mbar_try_wait(bar, parity)) return true;
+  for (int i = 0; i < kPolls; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < kPolls; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*ctl.abort) return false;
     if (globaltimer() - t0 > WAIT_LIMIT_NS) {
       *ctl.abort = 1;
@@ -343,10 +359,12 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 // As wait_phase, acquiring at cluster scope: for barriers that the peer CTA
 // of a pair arrives on (directly, or through a TMA or MMA completion).
 __device__ __forceinline__ bool wait_phase_cluster(uint32_t bar, uint32_t parity, const Ctl& ctl) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+  for (int i = 0; i < kPolls; ++i)
+    if (mbar_try_wait_cluster(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (true) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+    for (int i = 0; i < kPolls; ++i)
+      if (mbar_try_wait_cluster(bar, parity)) return true;
     if (*ctl.abort) return false;
     if (globaltimer() - t0 > WAIT_LIMIT_NS) {
       *ctl.abort = 1;
