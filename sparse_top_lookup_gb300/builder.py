@@ -15,7 +15,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkm.so")
 SOURCES = ["pkm_api.cu", "gather.cu", "lookup_simt.cu", "lookup_tc.cu", "lookup_2sm.cu", "lookup_merge.cu",
            "pkm_static.cu", "values_fp8.cu", "qnet.cu", "backward.cu", "flat.cu",
-           "ffn.cu", "distill.cu"]
+           "ffn.cu", "ffn_few.cu", "distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -31,6 +31,7 @@
 #include <atomic>
 #include <chrono>
 
+#include "ffn_common.cuh"
 #include "pkm_internal.cuh"
 #include "tc_common.cuh"
 
@@ -130,67 +131,6 @@ __device__ __forceinline__ bool seg_at(const Plan& p, int c, int i, Seg& s) {
   s.tile = c + i * p.clusters, s.k0 = 0, s.k1 = -1;
   return s.tile < p.whole;
 }
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 1 / (1 + exp(-x)), with x log2(e) given
-__device__ __forceinline__ float sigmoid2(float x2) { return rcp(1.0f + ex2(-x2)); }
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi): (1 + tanh v) / 2 = sigmoid(2 v)
-
-// act(g) and act'(g)
-template <int kAct>
-__device__ __forceinline__ float2 act_both(float g) {
-  if constexpr (kAct == PKM_ACT_SILU) {
-    const float s = sigmoid2(g * kLog2e), a = g * s;
-    return make_float2(a, fmaf(a, 1.0f - s, s));
-  } else if constexpr (kAct == PKM_ACT_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(g * 0.70710678f));
-    return make_float2(g * cdf, fmaf(g * 0.39894228f, ex2(g * g * (-0.5f * kLog2e)), cdf));
-  } else if constexpr (kAct == PKM_ACT_GELU_TANH) {
-    const float g2 = g * g;
-    const float s = sigmoid2(kTanh * kLog2e * g * fmaf(0.044715f, g2, 1.0f)), a = g * s;
-    return make_float2(a, fmaf(a * (1.0f - s), kTanh * fmaf(0.134145f, g2, 1.0f), s));
-  } else {
-    return make_float2(fmaxf(g, 0.0f), g > 0.0f ? 1.0f : 0.0f);
-  }
-}
-template <int kAct>
-__device__ __forceinline__ float act_fwd(float g) {
-  return act_both<kAct>(g).x;
-}
-// f(std::integral_constant-like tag) for the activation of a launch
-template <int kAct>
-struct ActTag {
-  static constexpr int value = kAct;
-};
-template <typename F>
-__device__ __forceinline__ void with_act(int act, F&& f) {
-  if (act == PKM_ACT_SILU)
-    f(ActTag<PKM_ACT_SILU>());
-  else if (act == PKM_ACT_GELU)
-    f(ActTag<PKM_ACT_GELU>());
-  else if (act == PKM_ACT_GELU_TANH)
-    f(ActTag<PKM_ACT_GELU_TANH>());
-  else
-    f(ActTag<PKM_ACT_RELU>());
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
 // A 32 x 32 block in shared memory as TMA stores it: rows of 64 bytes (bf16, 64-byte swizzle) or
 // of 128 (fp32, 128-byte swizzle); 16-byte piece `piece` of row `row`.
@@ -840,6 +780,9 @@ size_t gated_ffn_backward_workspace_bytes(int B, int F) {
 cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up,
                              const void* w_down, int B, int dim, int F, int act, void* workspace,
                              void* y, void* gate, void* up, int* status, cudaStream_t stream) {
+  if (B <= kFewTokens)
+    return launch_ffn_few(x, w_gate, w_up, w_down, B, dim, F, act, workspace, y, gate, up, status,
+                          stream);
   GemmArgs p = {};
   p.prods = 1;
   p.act = act;
@@ -876,7 +819,12 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
   p.g_in = static_cast<const __nv_bfloat16*>(gate);
   p.u_in = static_cast<const __nv_bfloat16*>(up);
   set_parts(p, ws + 3 * part, FM);
-  {  // dh = dy Wd, then dg, du and h
+  const bool few = B <= kFewTokens;
+  if (few) {
+    cudaError_t e = launch_ffn_few_backward(w_gate, w_up, w_down, gate, up, dy, B, dim, F, act, dg,
+                                            du, h, dx, status, stream);
+    if (e != cudaSuccess) return e;
+  } else {  // dh = dy Wd, then dg, du and h
     Prod& q = p.prod[0];
     q.segs = 1;
     q.M = B, q.N = F, q.K = dim, q.b_mn = 1;
@@ -910,11 +858,11 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
   };
   // longest tiles first: shorter ones fill the last rounds
   const bool first = 2 * (int64_t)F >= B;
-  if (dx && first && !input()) return cudaErrorInvalidValue;
+  if (dx && !few && first && !input()) return cudaErrorInvalidValue;
   if (dw_gate && (!weight(dg, F, x, dim, dw_gate) || !weight(du, F, x, dim, dw_up)))
     return cudaErrorInvalidValue;
   if (dw_down && !weight(dy, dim, h, F, dw_down)) return cudaErrorInvalidValue;
-  if (dx && !first && !input()) return cudaErrorInvalidValue;
+  if (dx && !few && !first && !input()) return cudaErrorInvalidValue;
   return p.prods ? launch_gemm<kStore>(p, b, stream) : cudaSuccess;
 }
 

@@ -1,0 +1,72 @@
+// Activations of the gated feed-forward block and bf16 packing, shared by its kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "../../include/pkm.h"
+
+namespace pkm {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + exp(-x)), with x log2(e) given
+__device__ __forceinline__ float sigmoid2(float x2) { return rcp(1.0f + ex2(-x2)); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi): (1 + tanh v) / 2 = sigmoid(2 v)
+
+// act(g) and act'(g)
+template <int kAct>
+__device__ __forceinline__ float2 act_both(float g) {
+  if constexpr (kAct == PKM_ACT_SILU) {
+    const float s = sigmoid2(g * kLog2e), a = g * s;
+    return make_float2(a, fmaf(a, 1.0f - s, s));
+  } else if constexpr (kAct == PKM_ACT_GELU) {
+    const float cdf = 0.5f * (1.0f + erff(g * 0.70710678f));
+    return make_float2(g * cdf, fmaf(g * 0.39894228f, ex2(g * g * (-0.5f * kLog2e)), cdf));
+  } else if constexpr (kAct == PKM_ACT_GELU_TANH) {
+    const float g2 = g * g;
+    const float s = sigmoid2(kTanh * kLog2e * g * fmaf(0.044715f, g2, 1.0f)), a = g * s;
+    return make_float2(a, fmaf(a * (1.0f - s), kTanh * fmaf(0.134145f, g2, 1.0f), s));
+  } else {
+    return make_float2(fmaxf(g, 0.0f), g > 0.0f ? 1.0f : 0.0f);
+  }
+}
+template <int kAct>
+__device__ __forceinline__ float act_fwd(float g) {
+  return act_both<kAct>(g).x;
+}
+// f(tag) with the activation of a launch as the tag's value
+template <int kAct>
+struct ActTag {
+  static constexpr int value = kAct;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
+  if (act == PKM_ACT_SILU)
+    f(ActTag<PKM_ACT_SILU>());
+  else if (act == PKM_ACT_GELU)
+    f(ActTag<PKM_ACT_GELU>());
+  else if (act == PKM_ACT_GELU_TANH)
+    f(ActTag<PKM_ACT_GELU_TANH>());
+  else
+    f(ActTag<PKM_ACT_RELU>());
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+}  // namespace pkm

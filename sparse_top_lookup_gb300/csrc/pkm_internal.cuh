@@ -168,6 +168,17 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
                                       void* dw_down, int grad_dtype, int* status,
                                       cudaStream_t stream);
 
+// Its products for few tokens (ffn_few.cu): the forward pass, and the backward pass up to dx (NULL:
+// not wanted); dg, du and h as in the workspace.
+constexpr int kFewTokens = 64;
+cudaError_t launch_ffn_few(const void* x, const void* w_gate, const void* w_up, const void* w_down,
+                           int B, int dim, int F, int act, void* h, void* y, void* gate, void* up,
+                           int* status, cudaStream_t stream);
+cudaError_t launch_ffn_few_backward(const void* w_gate, const void* w_up, const void* w_down,
+                                    const void* gate, const void* up, const void* dy, int B,
+                                    int dim, int F, int act, void* dg, void* du, void* h, void* dx,
+                                    int* status, cudaStream_t stream);
+
 // Distillation from a teacher's top logits (distill.cu); arguments as
 // pkm_distill's and pkm_distill_backward's, checked.
 cudaError_t launch_distill(const void* z, int dtype, int64_t ld, int B, int V, const int64_t* idx,

@@ -106,6 +106,15 @@ def test_forward(B, dim, F):
     check_forward(*inputs(B, dim, F, B + dim + F)[:4], act=ACTS[(B + F // 8) % 4])
 
 
+# few tokens: tiles of every height, shared by one CTA to eight, K tails, more tiles than SMs
+@pytest.mark.parametrize("B,dim,F", [(1, 1024, 4096), (16, 1024, 2048), (17, 2048, 520),
+                                     (48, 200, 5000), (64, 1032, 4104), (3, 64, 20480),
+                                     (2, 4096, 256), (63, 136, 136), (64, 8, 1000)])
+def test_few_tokens(B, dim, F):
+    check_forward(*inputs(B, dim, F, B + dim + F)[:4], act=ACTS[(dim // 8) % 4])
+    check_backward(B, dim, F, ACTS[(F // 8) % 4], seed=F)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("B", [3, 200])
 def test_activations(act, B):
@@ -228,8 +237,8 @@ def test_the_same_bits_every_time():
         assert torch.equal(forward(*a[:4], "gelu")[0], y)
 
 
-def test_on_another_stream_and_in_a_graph():
-    B, dim, F = 77, 128, 264
+@pytest.mark.parametrize("B,dim,F", [(77, 128, 264), (5, 128, 264), (33, 512, 1032)])
+def test_on_another_stream_and_in_a_graph(B, dim, F):
     x, wg, wu, wd, _ = inputs(B, dim, F, 4)
     want = forward(x, wg, wu, wd, "silu")[0].clone()
     s = torch.cuda.Stream()
