@@ -141,6 +141,10 @@ def _addr(x):
 def _stream(s):
     if s is None:
         import torch
+        # (the raw handle alone, where torch offers it: building a Stream object takes 3 us)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -318,12 +322,15 @@ def pkm_query_net(x, weight, B, dim, F, scale, shift, q, status=None, stream=Non
 
 def _dense(x, where):
     """x's address, for an argument that has to be contiguous (tensors and arrays are checked)."""
-    flags = getattr(x, "flags", None)
-    if (x.is_contiguous() if hasattr(x, "is_contiguous") else
-            flags is None or flags["C_CONTIGUOUS"]):
-        return _addr(x)
-    raise ValueError("%s: arguments are contiguous: got strides %r" % (where, x.stride()
-                     if hasattr(x, "stride") else x.strides))
+    if x is None or isinstance(x, int):
+        return x
+    if hasattr(x, "data_ptr"):
+        if x.is_contiguous():
+            return x.data_ptr()
+        raise ValueError("%s: arguments are contiguous: got strides %r" % (where, tuple(x.stride())))
+    if hasattr(x, "flags") and not x.flags["C_CONTIGUOUS"]:
+        raise ValueError("%s: arguments are contiguous: got strides %r" % (where, x.strides))
+    return _addr(x)
 
 
 def _rows(x, ld, where):

@@ -105,21 +105,27 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
 
   if (warp == 0) {
     // ------------------------------------------------ copies
+    // (all lanes run the loops, one is elected for each copy: see ffn.cu)
     auto weights = [&](uint32_t s, int k) {  // slabs from k on into stage s
       const int n = min(p.slabs, k_hi - k);
-      mbar_expect_tx(bar_full(s),
-                     (uint32_t)(n * ((kMode == kFewGate ? 2 : 1) * p.R * 128 + slab_t)));
+      if (elect_one())
+        mbar_expect_tx(bar_full(s),
+                       (uint32_t)(n * ((kMode == kFewGate ? 2 : 1) * p.R * 128 + slab_t)));
       for (int j = 0; j < n; ++j, ++k) {
         const int seg = k >= kb_seg ? 1 : 0, k0 = (k - seg * kb_seg) * WK;
         const uint32_t dst = ring + s * stage_bytes + j * slab_w;
         if (kMode == kFewGate) {
-          tma_load_2d(dst, &p.w[0], k0, m0, bar_full(s));
-          tma_load_2d(dst + 8192, &p.w[1], k0, m0, bar_full(s));
+          if (elect_one()) {
+            tma_load_2d(dst, &p.w[0], k0, m0, bar_full(s));
+            tma_load_2d(dst + 8192, &p.w[1], k0, m0, bar_full(s));
+          }
         } else if (p.w_mn) {
-          for (int i = 0; i < p.R; i += 64)
-            tma_load_2d(dst + i * 128, &p.w[seg], m0 + i, k0, bar_full(s));
+          if (elect_one()) {
+            tma_load_2d(dst, &p.w[seg], m0, k0, bar_full(s));
+            if (p.R > 64) tma_load_2d(dst + 8192, &p.w[seg], m0 + 64, k0, bar_full(s));
+          }
         } else {
-          tma_load_2d(dst, &p.w[seg], k0, m0, bar_full(s));
+          if (elect_one()) tma_load_2d(dst, &p.w[seg], k0, m0, bar_full(s));
         }
       }
     };
@@ -127,31 +133,24 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
       const int n = min(p.slabs, k_hi - k);
       for (int j = 0; j < n; ++j, ++k) {
         const int seg = k >= kb_seg ? 1 : 0, k0 = (k - seg * kb_seg) * WK;
-        tma_load_2d(ring + s * stage_bytes + p.slabs * slab_w + j * slab_t,
-                    &p.t[kMode == kFewGate ? 0 : seg], k0, 0, bar_full(s));
+        const uint32_t dst = ring + s * stage_bytes + p.slabs * slab_w + j * slab_t;
+        if (elect_one())
+          tma_load_2d(dst, &p.t[kMode == kFewGate ? 0 : seg], k0, 0, bar_full(s));
       }
     };
     // the ring's first filling: weights, then (once the kernel before this one is done) tokens
-    int first = 0;
-    for (int k = k_lo; k < k_hi && first < p.stages; k += p.slabs, ++first)
-      if (elect_one()) weights(first, k);
-    __syncwarp();
+    int issued = 0;
+    for (int k = k_lo; k < k_hi && issued < p.stages; k += p.slabs, ++issued) weights(issued, k);
     if (p.dependent) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
       asm volatile("fence.proxy.async;" ::: "memory");
     }
-    for (int i = 0; i < first; ++i)
-      if (elect_one()) tokens(i, k_lo + i * p.slabs);
-    __syncwarp();
-    int issued = first;
+    for (int i = 0; i < issued; ++i) tokens(i, k_lo + i * p.slabs);
     uint32_t s = 0, ph = 0;
     for (int k = k_lo + p.stages * p.slabs; k < k_hi; k += p.slabs, ++issued) {
       if (!__all_sync(0xffffffffu, wait_phase(bar_empty(s), ph, ctl))) break;
-      if (elect_one()) {
-        weights(s, k);
-        tokens(s, k);
-      }
-      __syncwarp();
+      weights(s, k);
+      tokens(s, k);
       if (++s == (uint32_t)p.stages) s = 0, ph ^= 1u;
     }
     // every copy lands before the ring is used for the sums (and before the CTA goes)
@@ -166,17 +165,17 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
       if (!__all_sync(0xffffffffu, wait_phase(bar_full(s), ph, ctl))) break;
       tc_fence_after();
       const int n = min(p.slabs, k_hi - k);
-      if (elect_one()) {
-        for (int j = 0; j < n; ++j) {
-          const uint32_t wa = ring + s * stage_bytes + j * slab_w;
-          const uint32_t ta = ring + s * stage_bytes + p.slabs * slab_w + j * slab_t;
-          const uint64_t wd = p.w_mn ? sw128_mn_desc(wa, 64 * WK * 2) : sw128_desc(wa);
-          const uint64_t td = sw128_desc(ta);
+      for (int j = 0; j < n; ++j) {
+        const uint32_t wa = ring + s * stage_bytes + j * slab_w;
+        const uint32_t ta = ring + s * stage_bytes + p.slabs * slab_w + j * slab_t;
+        const uint64_t wd = p.w_mn ? sw128_mn_desc(wa, 64 * WK * 2) : sw128_desc(wa);
+        const uint64_t td = sw128_desc(ta);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < WK / 16; ++kk)
             tc_mma(tmem, wd + w_step * kk, td + 2u * kk, idesc, (k - k_lo) + j + kk != 0);
+          if (j + 1 == n) tc_commit(bar_empty(s));
         }
-        tc_commit(bar_empty(s));
       }
       __syncwarp();
       if (++s == (uint32_t)p.stages) s = 0, ph ^= 1u;
@@ -284,7 +283,8 @@ void shape(FewArgs& p, int mode) {
     if (p.w_mn) R = R > 64 ? 128 : 64;
     if (R > r_max) R = r_max;
     const int64_t tiles = (p.M + R - 1) / R, rounds = (tiles + clusters - 1) / clusters;
-    const int64_t cost = rounds * R * per * 16 + lsh * R;
+    // bytes of a CTA, its tokens' too, and a slab's own cost (about 2 KB more)
+    const int64_t cost = rounds * per * ((mode == kFewGate ? 2 : 1) * R + p.npad + 16);
     if (best < 0 || cost < best) best = cost, p.R = R, p.lsh = lsh;
   }
   const int slab = (mode == kFewGate ? 8192 + p.R * 128 : p.R * 128) + p.npad * 128;
