@@ -96,6 +96,7 @@ struct GemmArgs {
   Prod prod[kMaxProds];
   CUtensorMap more[2];  // kGate (out: h): g, u; kDGate (out: dg): du, h
   int prods, act, keep;  // keep: kGate writes g and u
+  int dependent;         // on the launch before it
   Plan plan;
   const __nv_bfloat16 *g_in, *u_in;  // kDGate
   float4* parts;                // [stretch][CTA of the pair][column / 4][row], part_rows rows
@@ -267,6 +268,11 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   cluster_sync();  // both CTAs' barriers exist before any remote arrival
   const uint32_t tmem = s_tmem_base;
   const Ctl ctl{&s_abort, p.status};
+
+  // A call's later launches begin before the one before them has ended (programmatic dependent
+  // launch): everything up to here.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // The two issuing warps run their loops with all lanes and elect one only around what it
   // issues: with the loop in one lane's branch a step took 0.22 us more or less whatever it
@@ -707,17 +713,19 @@ Plan plan_of(const GemmArgs& p, int epi, int kN, int most, double* cost) {
 template <int kEpi, int kN>
 cudaError_t launch_tiles(GemmArgs& p, cudaStream_t stream, int* most) {
   auto kernel = ffn_gemm_kernel<kEpi, kN>;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(FTHREADS);
   cfg.dynamicSmemBytes = Tile<kN>::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.dependent && !most ? 2 : 1;
   if (most) {  // how many clusters run at one time
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Tile<kN>::kSmem);
@@ -798,6 +806,7 @@ cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up
   cudaError_t e = launch_gemm<kGate>(p, {{{w_gate, F, dim}, {w_up, F, dim}}}, stream);
   if (e != cudaSuccess) return e;
   q.N = dim, q.K = F;
+  p.dependent = 1;
   if (!operand(&q.a[0], workspace, B, F, false) || !result(&q.out, y, B, dim))
     return cudaErrorInvalidValue;
   return launch_gemm<kStore>(p, {{{w_down, dim, F}}}, stream);
@@ -835,6 +844,7 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
     if (e != cudaSuccess) return e;
   }
   // the rest in one launch
+  p.dependent = 1;
   const bool add = grad_dtype == PKM_F32;
   BOperand b[kMaxProds][2] = {};
   p.prods = 0;

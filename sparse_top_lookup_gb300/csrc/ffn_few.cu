@@ -36,10 +36,12 @@ enum FewMode { kFewGate, kFewStore, kFewDGate };
 
 struct FewArgs {
   CUtensorMap w[2], t[2];  // kFewGate: Wg and Wu against t[0]; else segment i: w[i] against t[i]
+  CUtensorMap t3_map[2];   // t as [K / 64][tokens][64]
   int M, T, K, segs;       // rows of weights, tokens, K of a segment
   int w_mn;                // weights stored with M contiguous (R is 64 or 128)
   int R, lsh;              // rows of a tile; log2 of the CTAs that share it
   int npad, slabs, stages; // tokens rounded up; slabs of a stage
+  int t3;                  // K is whole slabs: a stage's token slabs in one copy
   int act, keep, dependent;
   __nv_bfloat16 *out0, *out1, *out2;  // [T, M]: kFewGate h, g, u; kFewStore C; kFewDGate dg, du, h
   const __nv_bfloat16 *g_in, *u_in;   // kFewDGate
@@ -48,8 +50,9 @@ struct FewArgs {
 
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
   float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr)
-               : "memory");
+  // (volatile keeps it behind the barriers; no memory clobber, so that loads of several items
+  // can be in flight past the stores of the ones before)
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
   return v;
 }
 
@@ -131,11 +134,18 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
     };
     auto tokens = [&](uint32_t s, int k) {
       const int n = min(p.slabs, k_hi - k);
+      const uint32_t at = ring + s * stage_bytes + p.slabs * slab_w;
+      if (p.t3 && n == p.slabs && (k + n <= kb_seg || k >= kb_seg)) {
+        const int seg = k >= kb_seg ? 1 : 0;
+        if (elect_one())
+          tma_load_3d(at, &p.t3_map[kMode == kFewGate ? 0 : seg], 0, 0, k - seg * kb_seg,
+                      bar_full(s));
+        return;
+      }
       for (int j = 0; j < n; ++j, ++k) {
         const int seg = k >= kb_seg ? 1 : 0, k0 = (k - seg * kb_seg) * WK;
-        const uint32_t dst = ring + s * stage_bytes + p.slabs * slab_w + j * slab_t;
         if (elect_one())
-          tma_load_2d(dst, &p.t[kMode == kFewGate ? 0 : seg], k0, 0, bar_full(s));
+          tma_load_2d(at + j * slab_t, &p.t[kMode == kFewGate ? 0 : seg], k0, 0, bar_full(s));
       }
     };
     // the ring's first filling: weights, then (once the kernel before this one is done) tokens
@@ -183,6 +193,17 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
     if (elect_one()) tc_commit(bar_done);
     __syncwarp();
   }
+  // this CTA's share of the rows, two at a time, rows fastest
+  const int share = ((p.R + S - 1) >> p.lsh) + 1 & ~1;
+  const int r0 = rank * share, rows = min(share, min(p.R, p.M - m0) - r0);
+  const int half = (rows + 1) / 2, items = rows > 0 ? half * p.T : 0;
+  if (kMode == kFewDGate && warp >= 2)
+    for (int i = threadIdx.x - 64; i < items; i += 128) {
+      const int t = i / half;
+      const size_t o = (size_t)t * p.M + m0 + r0 + 2 * (i - t * half);
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.g_in + o));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.u_in + o));
+    }
   // every copy has landed and every MMA has read it: the ring takes the sums, [token][row]
   wait_phase(bar_done, 0, ctl);
   tc_fence_after();
@@ -201,15 +222,12 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
   tc_fence_before();
   __syncthreads();
   if (S > 1) cluster_sync();
-  // this CTA's share of the rows, two at a time, rows fastest
-  const int share = ((p.R + S - 1) >> p.lsh) + 1 & ~1;
-  const int r0 = rank * share, rows = min(share, min(p.R, p.M - m0) - r0);
-  if (rows > 0) {
-    const int half = (rows + 1) / 2;
-    for (int i = threadIdx.x; i < half * p.T; i += WTHREADS) {
+  if (items > 0) {
+    for (int i = threadIdx.x; i < items; i += WTHREADS) {
       const int t = i / half, r = r0 + 2 * (i - t * half);
       float2 a = make_float2(0.0f, 0.0f), b = a;
       const uint32_t at = ring + (t * 128 + r) * 4;
+#pragma unroll 4
       for (int c = 0; c < S; ++c) {
         const uint32_t from = S > 1 ? mapa_shared(at, c) : at;
         const float2 x = ld_cluster2(from);
@@ -235,8 +253,8 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
           put(p.out2, b.x, b.y);
         }
       } else {
-        const uint32_t g = *reinterpret_cast<const uint32_t*>(p.g_in + o);
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(p.u_in + o);
+        const uint32_t g = __ldg(reinterpret_cast<const uint32_t*>(p.g_in + o));
+        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p.u_in + o));
         with_act(p.act, [&](auto tag) {
           constexpr int kAct = decltype(tag)::value;
           const float2 x = act_both<kAct>(lo_bf16(g)), y = act_both<kAct>(hi_bf16(g));
@@ -264,6 +282,19 @@ bool encode_rows(CUtensorMap* m, const void* ptr, int rows, int cols, int box_co
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A [rows, cols] matrix, cols a multiple of 64, as [cols / 64][rows][64].
+bool encode_slabs(CUtensorMap* m, const void* ptr, int rows, int cols, int box_rows, int slabs) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {WK, (cuuint64_t)rows, (cuuint64_t)cols / WK};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, WK * 2};
+  const cuuint32_t box[3] = {WK, (cuuint32_t)box_rows, (cuuint32_t)slabs};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -299,12 +330,15 @@ cudaError_t launch_few(FewArgs& p, const void* w0, const void* w1, const void* t
                        cudaStream_t stream) {
   p.npad = (p.T + 15) / 16 * 16;
   shape(p, kMode);
+  p.t3 = p.K % WK == 0 && p.slabs > 1;
   const void *w[2] = {w0, w1}, *t[2] = {t0, t1};
   for (int i = 0; i < 2; ++i) {
     if (w[i] && !(p.w_mn ? encode_rows(&p.w[i], w[i], p.K, p.M, 64, WK)
                          : encode_rows(&p.w[i], w[i], p.M, p.K, WK, p.R)))
       return cudaErrorInvalidValue;
     if (t[i] && !encode_rows(&p.t[i], t[i], p.T, p.K, WK, p.npad)) return cudaErrorInvalidValue;
+    if (t[i] && p.t3 && !encode_slabs(&p.t3_map[i], t[i], p.T, p.K, p.npad, p.slabs))
+      return cudaErrorInvalidValue;
   }
   const int slab_w = kMode == kFewGate ? 8192 + p.R * 128 : p.R * 128;
   const int stage = p.slabs * (slab_w + p.npad * 128);
