@@ -44,22 +44,25 @@ constexpr int FM = 128;                   // rows per CTA (the pair's MMA takes 
 constexpr int FK = 64;                    // K per stage: one 128-byte swizzle row of bf16
 constexpr int FA_BYTES = FM * FK * 2;     // 16 KiB
 constexpr int FEPI_WARPS = 8;
-constexpr int FOUT_BYTES = 8192;          // of an epilogue warp: four buffers of 32 x 32 bf16
 constexpr int FTHREADS = 64 + 32 * FEPI_WARPS;
-// What goes with the tile's accumulator columns kN.
-template <int kN>
-struct Tile {
-  static constexpr int kB = kN / 2 * FK * 2;  // bytes of a B slab: each CTA holds half the columns
-  static constexpr int kStage = FA_BYTES + kB;
-  static constexpr int kStages = kN == 256 ? 5 : 6;
-  static constexpr int kSmem = kStages * kStage + FEPI_WARPS * FOUT_BYTES + 1024;  // + alignment
-  static_assert(kSmem + 512 <= 227 * 1024, "feed-forward shared memory");
-};
 
 enum Epi {
   kGate,   // accumulator columns: half of them g, the same half of u; writes h (and g, u)
   kStore,  // C in bf16, or (Prod::add32) added to an fp32 matrix
   kDGate   // accumulator: dh; reads g, u; writes dg, du, h
+};
+// What goes with the epilogue and the tile's accumulator columns kN.
+template <int kEpi, int kN>
+struct Tile {
+  static constexpr int kB = kN / 2 * FK * 2;  // bytes of a B slab: each CTA holds half the columns
+  static constexpr int kStage = FA_BYTES + kB;
+  // an epilogue warp's blocks of 32 x 32 bf16; kDGate: two sets of three (g, then dg; u, then du;
+  // h), which cost it one stage (a stage less is 5 % of a long product, measured)
+  static constexpr int kBlocks = kEpi == kDGate ? 6 : 4;
+  static constexpr int kOut = kBlocks * 2048;
+  static constexpr int kStages = (kN == 256 ? 5 : 6) - (kEpi == kDGate);
+  static constexpr int kSmem = kStages * kStage + FEPI_WARPS * kOut + 1024;  // + alignment
+  static_assert(kSmem + 768 <= 227 * 1024, "feed-forward shared memory");
 };
 
 // How a launch's tiles are split over its clusters.  The products' tiles are numbered one product
@@ -95,6 +98,7 @@ constexpr int kMaxProds = 4;
 struct GemmArgs {
   Prod prod[kMaxProds];
   CUtensorMap more[2];  // kGate (out: h): g, u; kDGate (out: dg): du, h
+  CUtensorMap in[2];    // kDGate: g, u
   int prods, act, keep;  // keep: kGate writes g and u
   int dependent;         // on the launch before it
   Plan plan;
@@ -188,6 +192,12 @@ __device__ __forceinline__ void add_block(const CUtensorMap* map, uint32_t buf, 
       : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void prefetch_block(const CUtensorMap* map, int col, int row) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(col), "r"(row)
+               : "memory");
+}
 // All but the last kPending stores of this thread have read their blocks.
 template <int kPending>
 __device__ __forceinline__ void blocks_read() {
@@ -220,9 +230,9 @@ template <int kEpi, int kN>
 __global__ void __launch_bounds__(FTHREADS, 1)
 ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   extern __shared__ unsigned char smem_raw[];
-  constexpr int FSTAGES = Tile<kN>::kStages, FSTAGE_BYTES = Tile<kN>::kStage,
-                FB_BYTES = Tile<kN>::kB;
-  __shared__ __align__(8) uint64_t bars[2 * FSTAGES + 4 + 1];
+  using Shape = Tile<kEpi, kN>;
+  constexpr int FSTAGES = Shape::kStages, FSTAGE_BYTES = Shape::kStage, FB_BYTES = Shape::kB;
+  __shared__ __align__(8) uint64_t bars[2 * FSTAGES + 4 + 1 + 2 * FEPI_WARPS];
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
 
@@ -251,6 +261,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       mbar_init(bar_tempty(b), 2 * FEPI_WARPS);   // leader: the epilogue warps of both CTAs
     }
     mbar_init(bar_done, 1);
+    for (int i = 0; i < 2 * FEPI_WARPS; ++i) mbar_init(bar_done + 8u * (1 + i), 1);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -382,8 +393,8 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
     // ------------------------------------------------ epilogue (both CTAs)
     const int quad = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t bufs = stages_u32 + FSTAGES * FSTAGE_BYTES + ew * FOUT_BYTES;
-    uint32_t nb = 0;  // next buffer of four
+    const uint32_t bufs = stages_u32 + FSTAGES * FSTAGE_BYTES + ew * Shape::kOut;
+    uint32_t nb = 0;  // next buffer of four; kDGate: bit k, the parity of set k's next loads
     Seg sg;
     for (int i = 0; seg_at(p.plan, slot, i, sg); ++i) {
       int tm, tn;
@@ -404,31 +415,24 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       };
       auto flag_at = [&](int r) { return p.flags + (size_t)(2 * r + rank) * FEPI_WARPS + ew; };
 
-      // kDGate: 16-byte pieces of g and u, four lanes to a row, asked for a chunk ahead
-      uint4 pg[kEpi == kDGate ? 4 : 1], pu[kEpi == kDGate ? 4 : 1];
+      // kDGate: chunk c's blocks of g and u into set (c / 32) & 1
+      const uint32_t bar_set = bar_done + 8u * (1 + 2 * ew);
       auto ask = [&](int c) {
-        if constexpr (kEpi == kDGate) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = row0 + 8 * j + (lane >> 2), cc = c + 8 * (lane & 3);
-            pg[j] = pu[j] = make_uint4(0, 0, 0, 0);
-            if (r < M && cc < cols) {
-              const size_t at = (size_t)r * N + col0 + cc;
-              pg[j] = __ldcs(reinterpret_cast<const uint4*>(p.g_in + at));
-              pu[j] = __ldcs(reinterpret_cast<const uint4*>(p.u_in + at));
-            }
-          }
-        }
+        const uint32_t k = (c >> 5) & 1, set = bufs + k * 3 * 2048;
+        blocks_read<0>();  // the set's stores are done with it
+        mbar_expect_tx(bar_set + 8u * k, 2 * 2048);
+        tma_load_2d(set, &p.in[0], col0 + c, row0, bar_set + 8u * k);
+        tma_load_2d(set + 2048, &p.in[1], col0 + c, row0, bar_set + 8u * k);
       };
-      if (kEpi == kDGate && sg.part < 0) {
-        if (in)  // the rest of the tile into L2 meanwhile (128 bytes at a time)
-          for (int c = 64; c < cols; c += 64) {
-            const size_t at = (size_t)row * N + col0 + c;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.g_in + at));
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.u_in + at));
-          }
-        ask(0);
+      if (kEpi == kDGate && sg.part < 0 && row0 < M && lane == 0) {
+        if (cols > 0) ask(0);
+        if (cols > 32) ask(32);
+        for (int c = 64; c < cols; c += 32) {  // the others into L2 meanwhile
+          prefetch_block(&p.in[0], col0 + c, row0);
+          prefetch_block(&p.in[1], col0 + c, row0);
+        }
       }
+      __syncwarp();
       if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_tfull(buf), use & 1u, ctl))) break;
       tc_fence_after();
       if (row0 < M && cols > 0) {
@@ -545,20 +549,16 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
                 if (lane == 0) add_block(&q.out, b0, gc, row0);
               }
             } else {
-              if (lane == 0) blocks_read<1>();
-              __syncwarp();
-              const uint32_t b0 = next_buf(), b1 = next_buf(), b2 = next_buf();
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                sts(at64(b0, 8 * j + (lane >> 2), lane & 3), pg[j]);
-                sts(at64(b1, 8 * j + (lane >> 2), lane & 3), pu[j]);
-              }
-              if (c + 32 < cols) ask(c + 32);
+              const uint32_t k = (c >> 5) & 1, b0 = bufs + k * 3 * 2048, b1 = b0 + 2048,
+                             b2 = b1 + 2048;
               sums(tc, v);
-              __syncwarp();
+              if (!__all_sync(0xffffffffu, wait_phase(bar_set + 8u * k, (nb >> k) & 1u, ctl))) break;
+              nb ^= 1u << k;
               float g[32], u[32];
               get_row(b0, lane, g);
               get_row(b1, lane, u);
+              // the other set for the next chunk (its stores, of the chunk before, are read by now)
+              if (lane == 0 && c >= 32 && c + 32 < cols) ask(c + 32);
               with_act(p.act, [&](auto tag) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -578,6 +578,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
                 store_block(&p.more[0], b1, gc, row0);
                 store_block(&p.more[1], b2, gc, row0);
               }
+              __syncwarp();
             }
           }
         }
@@ -722,13 +723,13 @@ cudaError_t launch_tiles(GemmArgs& p, cudaStream_t stream, int* most) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(FTHREADS);
-  cfg.dynamicSmemBytes = Tile<kN>::kSmem;
+  cfg.dynamicSmemBytes = Tile<kEpi, kN>::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = p.dependent && !most ? 2 : 1;
   if (most) {  // how many clusters run at one time
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Tile<kN>::kSmem);
+                                         Tile<kEpi, kN>::kSmem);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(2 * (sm_count() / 2));
     int n = 0;
@@ -838,7 +839,9 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
     q.segs = 1;
     q.M = B, q.N = F, q.K = dim, q.b_mn = 1;
     if (!operand(&q.a[0], dy, B, dim, false) || !result(&q.out, dg, B, F) ||
-        !result(&p.more[0], du, B, F) || !result(&p.more[1], h, B, F))
+        !result(&p.more[0], du, B, F) || !result(&p.more[1], h, B, F) ||
+        !result(&p.in[0], const_cast<void*>(gate), B, F) ||
+        !result(&p.in[1], const_cast<void*>(up), B, F))
       return cudaErrorInvalidValue;
     cudaError_t e = launch_gemm<kDGate>(p, {{{w_down, dim, F}}}, stream);
     if (e != cudaSuccess) return e;
