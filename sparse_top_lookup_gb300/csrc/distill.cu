@@ -94,16 +94,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&w);
 }
 
-// log of a positive s as a double good to about 1e-8: the exponent's part
-// exactly, the mantissa's (a value in [0.75, 1.5)) by logf.
-__device__ __forceinline__ double log_split(float s) {
+// A positive s as f 2^e, f in [0.75, 1.5): its log is e log 2 + logf(f), to about 1e-8 when the
+// two are added in 64 bits.
+struct Split {
   int e;
-  float f = frexpf(s, &e);  // [0.5, 1)
-  if (f < 0.75f) {
-    f *= 2.0f;
-    --e;
-  }
-  return (double)e * 0.6931471805599453 + (double)logf(f);
+  float f;
+};
+__device__ __forceinline__ Split split(float s) {
+  Split r;
+  r.f = frexpf(s, &r.e);  // [0.5, 1)
+  if (r.f < 0.75f) r.f *= 2.0f, --r.e;
+  return r;
 }
 
 // s * exp(m / T), s in the order of 1 (m = -inf: nothing yet, s is 0 or NaN).
@@ -130,6 +131,7 @@ struct DistillArgs {
   int lsh;            // log2 of a row's slices: the cluster's CTAs, or (kBwd) separate units
   int slots, chunk;   // ring of the CTA-per-slice form: slots of `chunk` 16-byte vectors
   float T;
+  double inv_t, t2;   // 1 / T, T^2
   const int64_t* idx;
   const float *teacher, *dloss;
   float *loss, *lse;  // kBwd reads lse
@@ -246,27 +248,33 @@ struct ListLoader {
   }
 };
 // By one warp: loss and lse of row b from its sum and its list (ls: what loading it returned).
-// The loss is a small difference of its terms: those are in 64 bits.
+//   log p_j - log q_j = ((t_j - tm) - (z_j - m)) / T + log(sum of q's terms / sum of p's)
+// The loss is a small difference of large logits, so each is taken from its maximum first; what is
+// left is good to fp32, and the logs and the last sums are in 64 bits (few of them: the GPU does
+// two 64-bit operations per SM and cycle, and with whole rows of terms in 64 bits they took
+// longer than rows of 2000 columns).
 __device__ void put_loss(const DistillArgs& a, int64_t b, const Sum& sum, const List& list,
                          const Sum& ls, int lane) {
-  const double inv_t = 1.0 / (double)a.T;
-  const double L = sum.s == 0.0f ? -INFINITY
-                                 : (sum.m == -INFINITY ? 0.0f : sum.m) * inv_t + log_split(sum.s);
-  double terms = 0.0;
-  if (ls.m != -INFINITY) {
-    const double o = L - ls.m * inv_t - log_split(ls.s);
+  float d = 0.0f;
+  if (ls.m != -INFINITY)
     for (int j = lane; j < a.k; j += 32) {
       const float p = list.p[j];
       if (p != 0.0f)  // (a NaN counts)
-        terms += list.z[j] == -INFINITY ? INFINITY
-                                        : p * (((double)list.t[j] - list.z[j]) * inv_t + o);
+        d += list.z[j] == -INFINITY ? INFINITY : p * ((list.t[j] - ls.m) - (list.z[j] - sum.m));
     }
-  }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) terms += __shfl_xor_sync(0xffffffffu, terms, o);
+  for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (lane == 0) {
-    a.loss[b] = (float)(terms * (double)a.T * a.T);
-    if (a.lse) a.lse[b] = (float)L;
+    constexpr double kLn2 = 0.6931471805599453;
+    const Split q = split(sum.s), p = split(ls.s);
+    const float log_q = logf(q.f);
+    double loss = 0.0;
+    if (ls.m != -INFINITY)
+      loss = sum.s == 0.0f ? (double)INFINITY
+                           : a.t2 * (d * a.inv_t + ((q.e - p.e) * kLn2 + (double)(log_q - logf(p.f))));
+    a.loss[b] = (float)loss;
+    if (a.lse)
+      a.lse[b] = sum.s == 0.0f ? -INFINITY : (float)(sum.m * a.inv_t + (q.e * kLn2 + log_q));
   }
 }
 
@@ -1001,6 +1009,7 @@ DistillArgs args_of(const void* z, int64_t ld, int B, int V, const int64_t* idx,
                     const float* teacher, int k, float T, int* status) {
   DistillArgs a = {};
   a.z = z, a.ld = ld, a.B = B, a.V = V, a.idx = idx, a.teacher = teacher, a.k = k, a.T = T;
+  a.inv_t = 1.0 / (double)T, a.t2 = (double)T * T;
   a.status = status;
   return a;
 }

@@ -336,17 +336,12 @@ struct Ctl {
   int* status;
 };
 
-// Polls between two looks at the clock: a wait that has to poll mostly ends without one.
-constexpr int kPolls = 64;
-
 // Waits for the phase of the given parity; false on time-out or abort.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const Ctl& ctl) {
-  for (int i = 0; i < kPolls; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (true) {
-    for (int i = 0; i < kPolls; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*ctl.abort) return false;
     if (globaltimer() - t0 > WAIT_LIMIT_NS) {
       *ctl.abort = 1;
@@ -359,12 +354,10 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
 // As wait_phase, acquiring at cluster scope: for barriers that the peer CTA
 // of a pair arrives on (directly, or through a TMA or MMA completion).
 __device__ __forceinline__ bool wait_phase_cluster(uint32_t bar, uint32_t parity, const Ctl& ctl) {
-  for (int i = 0; i < kPolls; ++i)
-    if (mbar_try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait_cluster(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (true) {
-    for (int i = 0; i < kPolls; ++i)
-      if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     if (*ctl.abort) return false;
     if (globaltimer() - t0 > WAIT_LIMIT_NS) {
       *ctl.abort = 1;
