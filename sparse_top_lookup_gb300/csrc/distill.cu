@@ -347,9 +347,27 @@ __device__ __forceinline__ void list_grad(const List& list, const DistillArgs& a
   }
 }
 
-// One vector of dz per lane: vector v (< end) of the row's out + head, from z's vector d.  `same`:
-// the rows of z and dz start alike within 16 bytes.  Otherwise the warp's 32 vectors go
-// through `stage` and out as whole words (bf16: with single elements at the ends).
+// Elements from p to the next 16-byte boundary.
+template <typename E>
+__device__ __forceinline__ int shift_of(const E* p) {
+  return (int)(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(E));
+}
+
+// 16 bytes from byte kBytes on of w and the vector behind it.
+template <int kBytes>
+__device__ __forceinline__ uint4 window(const uint32_t (&c)[8]) {
+  constexpr int i = kBytes / 4;
+  if constexpr (kBytes % 4 == 0)
+    return make_uint4(c[i], c[i + 1], c[i + 2], c[i + 3]);
+  else
+    return make_uint4(__funnelshift_r(c[i], c[i + 1], 16), __funnelshift_r(c[i + 1], c[i + 2], 16),
+                      __funnelshift_r(c[i + 2], c[i + 3], 16),
+                      __funnelshift_r(c[i + 3], c[i + 4], 16));
+}
+
+// One vector of dz per lane: vector v (< end) of the row's body, from z's vector d.  shift: from the
+// body to the next 16-byte boundary; where it is not 0 a lane stores the 16 aligned bytes that begin
+// in its vector and end in the next lane's, and the warp's first and last elements go singly.
 enum Form { kZero, kFast, kSlow };
 template <Form kForm>
 struct FormOf {
@@ -357,9 +375,9 @@ struct FormOf {
 };
 template <typename E, Form kForm, typename G>
 __device__ __forceinline__ void put_vector(E* body, int v, int end, const uint4& d, const G& q,
-                                           bool same, uint4* stage, int lane) {
+                                           int shift, int lane) {
   constexpr int kPer = El<E>::kPerVec;
-  uint32_t w[4];
+  uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (kForm == kZero) {
@@ -376,30 +394,38 @@ __device__ __forceinline__ void put_vector(E* body, int v, int end, const uint4&
         w[i] = pack2(q(z0), q(z1));
     }
   }
-  if (same) {
+  if (shift == 0) {
     if (v < end) __stcs(reinterpret_cast<uint4*>(body) + v, make_uint4(w[0], w[1], w[2], w[3]));
     return;
   }
-  const int first = v - lane;
-  const int n = min(32, end - first) * kPer;  // elements of the warp, may be <= 0
-  E* o = body + (int64_t)first * kPer;
-  stage[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-  __syncwarp();
-  const E* src = reinterpret_cast<const E*>(stage);
-  if constexpr (sizeof(E) == 4) {
-    for (int e = lane; e < n; e += 32) o[e] = src[e];
-  } else {
-    const int odd = (int)((reinterpret_cast<uintptr_t>(o) >> 1) & 1u);
-    for (int e = 2 * lane - odd; e < n; e += 64) {
-      if (e >= 0 && e + 1 < n)
-        *reinterpret_cast<__nv_bfloat162*>(o + e) = __nv_bfloat162(src[e], src[e + 1]);
-      else if (e >= 0)
-        o[e] = src[e];
-      else if (n > 0)
-        o[0] = src[0];
-    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+  const int last = min(32, end - (v - lane)) - 1;  // the warp's last vector, may be below 0
+  E* o = body + (int64_t)v * kPer;
+  if (lane < last) {
+    uint4 x;
+    if constexpr (kPer == 4)
+      x = shift == 1 ? window<4>(w) : shift == 2 ? window<8>(w) : window<12>(w);
+    else
+      switch (shift) {
+        case 1: x = window<2>(w); break;
+        case 2: x = window<4>(w); break;
+        case 3: x = window<6>(w); break;
+        case 4: x = window<8>(w); break;
+        case 5: x = window<10>(w); break;
+        case 6: x = window<12>(w); break;
+        default: x = window<14>(w); break;
+      }
+    __stcs(reinterpret_cast<uint4*>(o + shift), x);
   }
-  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    if ((lane == 0 && last >= 0 && e < shift) || (lane == last && e >= shift)) {
+      if constexpr (kPer == 4)
+        o[e] = __uint_as_float(w[e]);
+      else
+        reinterpret_cast<unsigned short*>(o)[e] = (unsigned short)(w[e / 2] >> (16 * (e & 1)));
+    }
 }
 
 // sum joined with the terms of vectors d, by one thread: 2^((z - m) c).
@@ -463,7 +489,6 @@ template <typename E, int kNV, int kMode>
 __global__ void __launch_bounds__(DTHREADS, kNV == 2 ? 4 : 3)
 distill_warp_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ uint4 s_stage[kMode == kFwd ? 1 : DTHREADS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float c = kLog2e / a.T;
   const List list(smem + (size_t)warp * kListBytes * a.kpad, a.kpad);
@@ -498,15 +523,14 @@ distill_warp_kernel(const DistillArgs a) {
       }();
       if (!zero) list_grad(list, a, q, g, lane, 32);
       E* out = static_cast<E*>(a.dz) + b * a.ld_d;
-      const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
+      const int shift = shift_of(out + row.head);
 #pragma unroll
       for (int j = 0; j < kNV; ++j) {
         const int v = j * 32 + lane;
-        uint4* stage = s_stage + warp * 32;
         if (zero)
-          put_vector<E, kZero>(out + row.head, v, row.nvec, d[j], q, same, stage, lane);
+          put_vector<E, kZero>(out + row.head, v, row.nvec, d[j], q, shift, lane);
         else
-          put_vector<E, kSlow>(out + row.head, v, row.nvec, d[j], q, same, stage, lane);
+          put_vector<E, kSlow>(out + row.head, v, row.nvec, d[j], q, shift, lane);
       }
       if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
       __syncwarp();  // the listed columns' values replace those of the row
@@ -525,7 +549,6 @@ template <typename E>
 __global__ void __launch_bounds__(DTHREADS + 32, 3)
 distill_backward_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ uint4 s_stage[DTHREADS];
   __shared__ Sum s_ls[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = kLog2e / a.T;
@@ -563,14 +586,13 @@ distill_backward_kernel(const DistillArgs a) {
     const bool zero = g == 0.0f || s_ls[par].m == -INFINITY;
     if (!zero) list_grad(list, a, q, g, tid, DTHREADS);
     E* out = static_cast<E*>(a.dz) + b * a.ld_d;
-    const bool same = (reinterpret_cast<uintptr_t>(out + row.head) & 15u) == 0;
+    const int shift = shift_of(out + row.head);
     auto put = [&](auto form) {
 #pragma unroll
       for (int j = 0; j < kBwdVecs; ++j) {
         const int v = row.v0 + j * DTHREADS + tid;
         if (v - lane >= row.v1) break;
-        put_vector<E, decltype(form)::value>(out + row.head, v, row.v1, d[j], q, same,
-                                             s_stage + warp * 32, lane);
+        put_vector<E, decltype(form)::value>(out + row.head, v, row.v1, d[j], q, shift, lane);
       }
     };
     if (zero)
@@ -629,18 +651,17 @@ struct Geo {
   float g;   // dloss * T
   int n;     // vectors of the slice
   int head, nvec, v0, ends;  // as in Row; ends: elements outside the vectors (slice 0: else 0)
-  int same;  // z's and dz's rows start alike within 16 bytes
+  int shift;  // elements from dz's body to the next 16-byte boundary
 };
 
 constexpr int kData = DWARPS, kListWarps = 2;
 constexpr int kStreamThreads = 32 * (kData + kListWarps + 1);
 template <typename E, int kMode>
-__global__ void __launch_bounds__(kStreamThreads, kMode == kTrain ? 2 : 3)
+__global__ void __launch_bounds__(kStreamThreads, 3)
 distill_stream_kernel(const DistillArgs a) {
   using namespace tc;
   constexpr int kThreads = kData * 32, kPer = El<E>::kPerVec;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint4 s_stage[kMode == kFwd ? 1 : kThreads];
   __shared__ Sum s_warp[kCopies][kData];
   __shared__ __align__(8) Sum s_slice[kCopies][kMaxSlices];
   __shared__ float s_tm[kCopies];   // largest t of the list, -inf if it is empty
@@ -699,7 +720,7 @@ distill_stream_kernel(const DistillArgs a) {
         geo.n = row.v1 - row.v0;
         geo.head = row.head, geo.nvec = row.nvec, geo.v0 = row.v0;
         geo.ends = slice == 0 ? a.V - row.nvec * kPer : 0;
-        geo.same = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+        geo.shift = shift_of(out);
         int v = 0;
         do {  // (a slice without vectors is one empty chunk)
           if (!(ok = wait_phase(bar_empty(s), ph, ctl))) break;
@@ -823,21 +844,21 @@ distill_stream_kernel(const DistillArgs a) {
       const Grad q = grad_of(sum_of(i - 1), g, c);
       E* body = geo.body;
       const int total = geo.n;
-      const bool same = geo.same;
+      const int shift = geo.shift;
       for (int v = 0; v < total || v == 0; v += chunk) {
         const uint4* src = ring + (size_t)s2 * chunk;
         const int n = min(chunk, total - v);
         E* out = body + (int64_t)v * kPer;
         auto put = [&](auto form) {
           constexpr Form kForm = decltype(form)::value;
-          if (same) {
+          if (shift == 0) {
 #pragma unroll 4
             for (int at = tid; at < n; at += kThreads)
-              put_vector<E, kForm>(out, at, n, src[at], q, true, nullptr, lane);
+              put_vector<E, kForm>(out, at, n, src[at], q, 0, lane);
           } else {
             for (int at = tid; at - lane < n; at += kThreads)
-              put_vector<E, kForm>(out, at, n, at < n ? src[at] : masked_vector<E>(), q, false,
-                                   s_stage + warp * 32, lane);
+              put_vector<E, kForm>(out, at, n, at < n ? src[at] : masked_vector<E>(), q, shift,
+                                   lane);
           }
         };
         if (zero)
