@@ -268,7 +268,11 @@ __device__ __forceinline__ void merge_cta(const float* __restrict__ list_v,
   if (!valid) return;
   int64_t* ip = idx + (size_t)pair * k;
   float* wp = w + (size_t)pair * k;
-  auto flat_of = [&](uint32_t pc) { return (int64_t)col1((int)(pc >> 5)) * n + col2((int)(pc & 31)); };
+  // (masked to the lists' length: after a selection that gave up, the lists hold whatever the
+  // scratch held, NaNs among it, places stay empty and a code may be anything)
+  auto flat_of = [&](uint32_t pc) {
+    return (int64_t)col1((int)((pc >> 5) & (KL - 1))) * n + col2((int)(pc & (KL - 1)));
+  };
   uint32_t held = nsurv < (uint32_t)kCap ? nsurv : (uint32_t)kCap;
   // a tie at x (more than KL pairs reach it): the pairs at x are ranked by
   // flat index after the larger sums, and those ranked KL or later dropped
@@ -288,6 +292,8 @@ __device__ __forceinline__ void merge_cta(const float* __restrict__ list_v,
         surv_push<kThreads * 4, kCap * kThreads * 4>(va2, held, va_end, xi + v1[KL + j], x,
                                                      (uint32_t)(i * 32 + j));
     }
+    // (fewer than KL, if V is what the lists give: not after a selection that gave up)
+    held = held < (uint32_t)kCap ? held : (uint32_t)kCap;
   }
   // Each held survivor's output place is the number of larger sums (its
   // pair code goes to that place's slot of this thread's column); branch
