@@ -133,7 +133,9 @@ __device__ __forceinline__ bool seg_at(const Plan& p, int c, int i, Seg& s) {
     }
     i -= n;
   }
-  s.tile = c + i * p.clusters, s.k0 = 0, s.k1 = -1;
+  // (every other round backwards: the clusters with the longest tiles of a launch, its first,
+  // are the last to get a second one)
+  s.tile = i * p.clusters + (i & 1 ? p.clusters - 1 - c : c), s.k0 = 0, s.k1 = -1;
   return s.tile < p.whole;
 }
 
@@ -681,8 +683,8 @@ Plan plan_of(const GemmArgs& p, int epi, int kN, int most, double* cost) {
     pl.kb = kb;
   }
   if (rows > 2 * FM) rows = 2 * FM;
-  // a slab of 128 columns takes about 0.6 of one of 256 (both operands' bytes: 24 of 32 KB)
-  const double slab = kN == 256 ? 1.0 : 0.6;
+  // a slab of 128 columns takes about 0.66 of one of 256 (4096 x 1024 x 4096: 52 us against 39)
+  const double slab = kN == 256 ? 1.0 : 0.66;
   pl.clusters = pl.tiles < most ? pl.tiles : most;
   pl.whole = pl.tiles;
   double rounds;  // of the longest tile
@@ -692,14 +694,14 @@ Plan plan_of(const GemmArgs& p, int epi, int kN, int most, double* cost) {
   else  // tiles of several lengths even out
     rounds = (double)slabs / most + 0.5 * longest > longest ? (double)slabs / most + 0.5 * longest
                                                              : longest;
-  // Cutting (one product): a tile into up to 4.  A part costs about 10 slabs' time to write, to
-  // wait for and to read, for all 256 rows and columns, each further one 3.
+  // Cutting (one product): a tile into up to 4.  Parts cost about 6 us, 24 slabs' time, to write,
+  // to wait for and to read (200 tokens, F = 8192, dim = 2048: 30 us whole, 20 cut in four).
   if (p.prods == 1 && left) {
     int64_t w = ((int64_t)left * pl.kb + most - 1) / most;
     if (w < (pl.kb + 3) / 4) w = (pl.kb + 3) / 4;
     const int parts = (int)((pl.kb + w - 1) / w);  // and one more where stretches straddle tiles
     const double area = (rows / (2.0 * FM)) * (kN / 256.0);
-    const double extra = 4 + (6 + 3 * parts) * area;
+    const double extra = 14 + (6 + 3 * parts) * area;
     if (w * slab + extra < pl.kb * slab && (int64_t)left * pl.kb < INT32_MAX / 2) {
       pl.w = (int)w;
       pl.whole = pl.tiles - left;
