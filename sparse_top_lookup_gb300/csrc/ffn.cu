@@ -66,17 +66,18 @@ struct Tile {
 };
 
 // How a launch's tiles are split over its clusters.  The products' tiles are numbered one product
-// after the other.  The first `whole` of them, one per cluster and round, are done whole.  The
-// slabs of those left, of kb slabs each, are laid end to end and cut into stretches of w: a
-// stretch begins with the end of a tile (its cluster writes those sums to memory: a part) and
+// after the other.  `whole` of them, from tile whole0 on, are done whole, one per cluster and
+// round.  `cut` of them, from cut0 on, of kb slabs each, are laid end to end and cut into
+// stretches of w slabs (what a single product leaves after its last full round; or a launch's
+// first product, when its few tiles are much longer than the others): a stretch begins with the end of a tile (its cluster writes those sums to memory: a part) and
 // goes on with the beginning of the next, whose cluster adds the other stretches' parts, waits
 // for them if it must, and writes the tile.  Stretches are done first, and a cluster waits only
 // for clusters of lower numbers, which start before it and never wait before they have written
 // their part.
 struct Plan {
-  int tiles, kb, clusters;
-  int whole;   // tiles done whole
-  int w;       // slabs of a stretch, 0: no tile is cut (every tile is whole)
+  int clusters;
+  int whole0, whole;
+  int cut0, cut, kb, w;  // cut 0: no tile is cut
 };
 struct Seg {
   int tile, k0, k1;  // k1 < 0: all of the tile's slabs
@@ -113,19 +114,19 @@ struct GemmArgs {
 // Segment i of cluster c; false past the last.
 __device__ __forceinline__ bool seg_at(const Plan& p, int c, int i, Seg& s) {
   s.part = -1, s.parts = 0, s.first = 0;
-  if (p.w) {
+  if (p.cut) {
     const int r = p.clusters - 1 - c;  // a tile's later stretches belong to lower clusters
-    const int total = (p.tiles - p.whole) * p.kb;
+    const int total = p.cut * p.kb;
     const int lo = min(r * p.w, total), hi = min(lo + p.w, total);
     const int t0 = lo / p.kb;
     const int mid = lo == t0 * p.kb ? lo : min(hi, (t0 + 1) * p.kb);  // where a tile begins
     const int n = (lo < mid) + (mid < hi);
     if (i < n) {
       if (i == 0 && lo < mid) {
-        s.tile = p.whole + t0, s.k0 = lo - t0 * p.kb, s.k1 = mid - t0 * p.kb, s.part = r;
+        s.tile = p.cut0 + t0, s.k0 = lo - t0 * p.kb, s.k1 = mid - t0 * p.kb, s.part = r;
       } else {
         const int t = mid / p.kb;
-        s.tile = p.whole + t, s.k0 = 0, s.k1 = hi - mid;
+        s.tile = p.cut0 + t, s.k0 = 0, s.k1 = hi - mid;
         s.first = r + 1;
         s.parts = ((t + 1) * p.kb - 1) / p.w - r;
       }
@@ -135,8 +136,9 @@ __device__ __forceinline__ bool seg_at(const Plan& p, int c, int i, Seg& s) {
   }
   // (every other round backwards: the clusters with the longest tiles of a launch, its first,
   // are the last to get a second one)
-  s.tile = i * p.clusters + (i & 1 ? p.clusters - 1 - c : c), s.k0 = 0, s.k1 = -1;
-  return s.tile < p.whole;
+  const int t = i * p.clusters + (i & 1 ? p.clusters - 1 - c : c);
+  s.tile = p.whole0 + t, s.k0 = 0, s.k1 = -1;
+  return t < p.whole;
 }
 
 // A 32 x 32 block in shared memory as TMA stores it: rows of 64 bytes (bf16, 64-byte swizzle) or
@@ -665,48 +667,58 @@ unsigned long long next_epoch() {
   return e ? e : n.fetch_add(1, std::memory_order_relaxed);
 }
 
-// The products of p in tiles of kN columns over at most `most` clusters, and how long that takes,
-// in slabs of a 256-column tile.
+// The products of p in tiles of kN columns over at most `most` clusters, and about how long that
+// takes, in slabs of a 256-column tile.
 Plan plan_of(const GemmArgs& p, int epi, int kN, int most, double* cost) {
   const int tile_n = epi == kGate ? kN / 2 : kN;
   Plan pl = {};
   int64_t slabs = 0;
-  int rows = 0, longest = 0;
+  int tiles = 0, longest = 0, first_tiles = 0, first_kb = 0, others = 0;
   for (int i = 0; i < p.prods; ++i) {
     const Prod& q = p.prod[i];
     const int t = (q.M + 2 * FM - 1) / (2 * FM) * ((q.N + tile_n - 1) / tile_n);
     const int kb = (q.K + FK - 1) / FK * q.segs;
-    pl.tiles += t;
+    tiles += t;
     slabs += (int64_t)t * kb;
-    rows = q.M > rows ? q.M : rows;
     longest = kb > longest ? kb : longest;
-    pl.kb = kb;
+    if (i == 0)
+      first_tiles = t, first_kb = kb;
+    else
+      others = kb > others ? kb : others;
   }
-  if (rows > 2 * FM) rows = 2 * FM;
   // a slab of 128 columns takes about 0.66 of one of 256 (4096 x 1024 x 4096: 52 us against 39)
   const double slab = kN == 256 ? 1.0 : 0.66;
-  pl.clusters = pl.tiles < most ? pl.tiles : most;
-  pl.whole = pl.tiles;
-  double rounds;  // of the longest tile
-  const int left = pl.tiles % most;
+  pl.clusters = tiles < most ? tiles : most;
+  pl.whole = tiles;
+  double rounds;  // in slabs; tiles of several lengths even out
   if (p.prods == 1)
-    rounds = (double)((pl.tiles + most - 1) / most) * pl.kb;
-  else  // tiles of several lengths even out
-    rounds = (double)slabs / most + 0.5 * longest > longest ? (double)slabs / most + 0.5 * longest
-                                                             : longest;
-  // Cutting (one product): a tile into up to 4.  Parts cost about 6 us, 24 slabs' time, to write,
-  // to wait for and to read (200 tokens, F = 8192, dim = 2048: 30 us whole, 20 cut in four).
-  if (p.prods == 1 && left) {
-    int64_t w = ((int64_t)left * pl.kb + most - 1) / most;
-    if (w < (pl.kb + 3) / 4) w = (pl.kb + 3) / 4;
-    const int parts = (int)((pl.kb + w - 1) / w);  // and one more where stretches straddle tiles
-    const double area = (rows / (2.0 * FM)) * (kN / 256.0);
-    const double extra = 14 + (6 + 3 * parts) * area;
-    if (w * slab + extra < pl.kb * slab && (int64_t)left * pl.kb < INT32_MAX / 2) {
-      pl.w = (int)w;
-      pl.whole = pl.tiles - left;
-      rounds -= pl.kb - w - extra / slab;
-      pl.clusters = pl.whole ? most : (int)(((int64_t)left * pl.kb + w - 1) / w);
+    rounds = (double)((tiles + most - 1) / most) * longest;
+  else
+    rounds = (double)slabs / most + 0.5 * others > longest ? (double)slabs / most + 0.5 * others
+                                                           : longest;
+  // Cutting: a tile into up to 4.  Parts cost about 6 us, 24 slabs' time, to write, to wait for
+  // and to read (200 tokens, F = 8192, dim = 2048: 30 us whole, 20 cut in four).
+  const int cut = p.prods == 1 ? tiles % most : first_tiles, kb = first_kb;
+  if (cut && (int64_t)cut * kb < INT32_MAX / 2) {
+    int64_t w = ((int64_t)cut * kb + most - 1) / most;
+    if (w < (kb + 3) / 4) w = (kb + 3) / 4;
+    const int parts = (int)((kb + w - 1) / w);  // and one more where stretches straddle tiles
+    const int rows = p.prod[0].M < 2 * FM ? p.prod[0].M : 2 * FM;
+    const double extra = (14 + (6 + 3 * parts) * (rows / (2.0 * FM)) * (kN / 256.0)) / slab;
+    double with;  // rounds, if it is cut
+    if (p.prods == 1) {
+      with = rounds - kb + w + extra;
+    } else {
+      const double rest = (double)(slabs - (int64_t)cut * kb) / most + 0.5 * others;
+      with = w + extra + (rest > others ? rest : others);
+    }
+    if (w < kb && with < rounds) {
+      rounds = with;
+      pl.cut = cut, pl.kb = kb, pl.w = (int)w;
+      pl.whole = tiles - cut;
+      pl.cut0 = p.prods == 1 ? pl.whole : 0;
+      pl.whole0 = p.prods == 1 ? 0 : cut;
+      pl.clusters = pl.whole ? most : (int)(((int64_t)cut * kb + w - 1) / w);
     }
   }
   *cost = rounds * slab;

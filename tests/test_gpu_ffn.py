@@ -115,6 +115,18 @@ def test_few_tokens(B, dim, F):
     check_backward(B, dim, F, ACTS[(F // 8) % 4], seed=F)
 
 
+# few tiles of long products: tiles cut along K, and joined in a fixed order
+@pytest.mark.parametrize("B,dim,F", [(200, 256, 8192), (129, 264, 6000), (513, 136, 5000),
+                                     (150, 1024, 4096), (300, 2048, 2048)])
+def test_cut_tiles(B, dim, F):
+    x, wg, wu, wd, _ = inputs(B, dim, F, B + dim)
+    check_forward(x, wg, wu, wd, "silu")
+    check_backward(B, dim, F, "gelu_tanh", seed=F)
+    check_backward(B, dim, F, "silu", seed=F, grad_dtype=pk.PKM_F32)
+    y = forward(x, wg, wu, wd, "silu")[0].clone()
+    assert torch.equal(forward(x, wg, wu, wd, "silu")[0], y)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("B", [3, 200])
 def test_activations(act, B):
