@@ -461,20 +461,20 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
             asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(flag_at(sg.part)), "l"(p.epoch)
                          : "memory");
         } else {
-          for (int r = sg.first; r < sg.first + sg.parts; ++r) {
-            if (lane == 0) {
-              const unsigned long long t0 = globaltimer();
+          for (int r0 = 0; r0 < sg.parts; r0 += 32) {  // a lane waits for each part
+            if (r0 + lane < sg.parts) {
+              unsigned long long* flag = flag_at(sg.first + r0 + lane);
+              const unsigned long long begun = globaltimer();
               unsigned long long f;
               do {
-                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(f) : "l"(flag_at(r))
-                             : "memory");
-                if (f != p.epoch && globaltimer() - t0 > WAIT_LIMIT_NS) {
+                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(f) : "l"(flag) : "memory");
+                if (f != p.epoch && globaltimer() - begun > WAIT_LIMIT_NS) {
                   s_abort = 1;
                   atomicExch(p.status, PKM_ERR_TIMEOUT);
                   break;
                 }
               } while (f != p.epoch && !*ctl.abort);
-              *flag_at(r) = 0;  // the next launch with this workspace starts afresh
+              *flag = 0;  // the next launch with this workspace starts afresh
             }
             __syncwarp();
           }
