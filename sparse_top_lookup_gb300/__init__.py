@@ -322,24 +322,29 @@ def pkm_query_net(x, weight, B, dim, F, scale, shift, q, status=None, stream=Non
 
 def _dense(x, where):
     """x's address, for an argument that has to be contiguous (tensors and arrays are checked)."""
-    if x is None or isinstance(x, int):
-        return x
-    if hasattr(x, "data_ptr"):
+    if x is None:
+        return None
+    try:
         if x.is_contiguous():
             return x.data_ptr()
-        raise ValueError("%s: arguments are contiguous: got strides %r" % (where, tuple(x.stride())))
-    if hasattr(x, "flags") and not x.flags["C_CONTIGUOUS"]:
-        raise ValueError("%s: arguments are contiguous: got strides %r" % (where, x.strides))
-    return _addr(x)
+    except AttributeError:  # no tensor
+        if hasattr(x, "flags") and not x.flags["C_CONTIGUOUS"]:
+            raise ValueError("%s: arguments are contiguous: got strides %r" % (where, x.strides))
+        return _addr(x)
+    raise ValueError("%s: arguments are contiguous: got strides %r" % (where, tuple(x.stride())))
 
 
 def _rows(x, ld, where):
     """x's address, for a matrix whose rows are contiguous and ld elements apart."""
-    if hasattr(x, "stride") and x.dim() == 2 and (
-            (x.size(1) > 1 and x.stride(1) != 1) or (x.size(0) > 1 and x.stride(0) != ld)):
+    try:
+        st = x.stride()
+    except AttributeError:  # no tensor
+        return _addr(x)
+    if len(st) == 2 and st != (ld, 1) and (
+            (x.size(1) > 1 and st[1] != 1) or (x.size(0) > 1 and st[0] != ld)):
         raise ValueError("%s: rows are contiguous and ld elements apart: got strides %r, ld %d"
-                         % (where, tuple(x.stride()), ld))
-    return _addr(x)
+                         % (where, tuple(st), ld))
+    return x.data_ptr()
 
 
 def pkm_gated_ffn_workspace_bytes(B, dim, F):
