@@ -14,9 +14,16 @@
 // sum); short rows are held in the registers of a warp each.
 //
 // Softmax arithmetic is in powers of two: with c = log2(e) / T and the
-// largest logit m, the terms are 2^((z - m) c).  The difference comes first:
-// logits at the type's lowest value, as some masks have them, would overflow
-// in z c.
+// largest logit m, the terms are 2^((z - m) c).  Where m c is in range they
+// are formed as 2^(z c - r), r = rn(m c), one instruction less; where it is
+// not (rows whose every logit is a mask's lowest value) the difference comes
+// first.
+//
+// Measured, GB/s of logits read and dz written (a copy reaches 6802): training step fp32 4096 x
+// 65536 6600 (97 %), bf16 4096 x 131072 with lists of 64 5440 (80 %), with lists of 4 5890; loss
+// alone, bf16 4096 x 131072 6360 (94 %).  A byte of bf16 logits costs twice the arithmetic of fp32
+// ones: that, not HBM, bounds the bf16 training step (issue slots 64 % busy, the same code at fp32
+// is at the copy's rate).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -484,7 +491,8 @@ __device__ __forceinline__ uint4 masked_vector() {
 }
 
 // Short rows: a warp each, which keeps the row in registers, kNV vectors per lane, between its
-// sum and its gradient.
+// sum and its gradient.  Bound by the lists and the loss's logs more than by the logits: training
+// step bf16 8192 x 2000 27 us captured (65 MB), 8192 x 200 15.5 us (6.6 MB).
 template <typename E, int kNV, int kMode>
 __global__ void __launch_bounds__(DTHREADS, kNV == 2 ? 4 : 3)
 distill_warp_kernel(const DistillArgs a) {
@@ -543,7 +551,10 @@ distill_warp_kernel(const DistillArgs a) {
 }
 
 // kBwd: units of 8 vectors per data thread, each by itself, in registers.  A list warp is a unit
-// ahead with the lists (two copies: a unit's is in use until the next unit's barrier).
+// ahead with the lists (two copies: a unit's is in use until the next unit's barrier).  lse is
+// known, so nothing is exchanged and units need no ring: loads of 8 vectors per thread and three
+// CTAs per SM cover HBM's latency.  fp32 1500 x 50257 99 us (6090 GB/s, 90 %), bf16 4096 x 131072
+// 370 (5810; lists of 4: 338).
 constexpr int kBwdVecs = 8;
 template <typename E>
 __global__ void __launch_bounds__(DTHREADS + 32, 3)

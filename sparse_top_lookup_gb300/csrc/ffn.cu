@@ -17,8 +17,16 @@
 // 128-byte swizzle.  What differs is the epilogue (Epi): each warp turns 32
 // columns of its 32 rows at a time into bf16 in its own shared-memory buffers
 // and stores them by TMA (a thread's own 64 bytes of a row, stored directly,
-// touch 32 lines per instruction: the gate's epilogue took longer than its
-// product that way).
+// touch 32 lines per instruction: the forward gate took 745 us at 16384 x 2048 x
+// 8192 that way, 600 this way).
+//
+// Bound by the tensor pipe in long products: 92 to 95 % busy in the gate and in the backward
+// pass's last four at 4096 x 2048 x 8192, 81 % in the down projection (128 tiles on 74 clusters),
+// at the clock that 1400 W leaves.  A tile of 256 x 256 writes and reads shared memory at nearly
+// the rate that it has, so what an epilogue moves through it costs time: the backward gate's
+// (five tensors, 20 KB per 32 x 32 block) leaves the tensor pipe 53 % busy.  Its other forms
+// took longer: g and u through registers 469 us at 16384 x 2048 x 8192, h stored directly 508, this
+// one 432.
 //
 // One launch takes several products (the backward pass's last four), so that
 // small ones fill the GPU together.  Work is split evenly over the clusters
@@ -69,9 +77,10 @@ struct Tile {
 // after the other.  `whole` of them, from tile whole0 on, are done whole, one per cluster and
 // round.  `cut` of them, from cut0 on, of kb slabs each, are laid end to end and cut into
 // stretches of w slabs (what a single product leaves after its last full round; or a launch's
-// first product, when its few tiles are much longer than the others): a stretch begins with the end of a tile (its cluster writes those sums to memory: a part) and
-// goes on with the beginning of the next, whose cluster adds the other stretches' parts, waits
-// for them if it must, and writes the tile.  Stretches are done first, and a cluster waits only
+// first product, when its few tiles are much longer than the others): a stretch begins with the
+// end of a tile (its cluster writes those sums to memory: a part) and goes on with the beginning
+// of the next, whose cluster adds the other stretches' parts, waits for them if it must, and
+// writes the tile.  Stretches are done first, and a cluster waits only
 // for clusters of lower numbers, which start before it and never wait before they have written
 // their part.
 struct Plan {

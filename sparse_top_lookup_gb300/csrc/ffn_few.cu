@@ -13,7 +13,12 @@
 // Bound by HBM, and at one token by latency: a ring of about 100 KB per SM keeps 15 MB of weights
 // in flight, and the second kernel of a call starts while the first one runs (programmatic
 // dependent launch; both fit on an SM): it fills its ring with weights and waits for the first
-// only before it loads the tokens' rows.
+// only before it loads the tokens' rows.  Rings of 64 and 180 KB: 11.4 and 17 us at one token of
+// 1024 x 4096 (captured; this one 12), 31 and 42 at 37 of 2048 x 8192 (this one 28).
+//
+// Measured at 37 tokens of 2048 x 8192 (100 MB of weights, 14.8 us at the copy's rate): 28 us
+// captured.  The gate's weights stream from 2.4 to 15 us at 5.4 TB/s and its results are out at
+// 17.5; the second kernel's tokens are there at 20, its products done at 25.5, its results out at 28.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
