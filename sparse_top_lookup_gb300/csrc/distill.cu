@@ -20,10 +20,8 @@
 // first.
 //
 // Measured, GB/s of logits read and dz written (a copy reaches 6802): training step fp32 4096 x
-// 65536 6600 (97 %), bf16 4096 x 131072 with lists of 64 5440 (80 %), with lists of 4 5890; loss
-// alone, bf16 4096 x 131072 6360 (94 %).  A byte of bf16 logits costs twice the arithmetic of fp32
-// ones: that, not HBM, bounds the bf16 training step (issue slots 64 % busy, the same code at fp32
-// is at the copy's rate).
+// 65536 6470 (95 %), bf16 4096 x 131072 with lists of 64 6270 (92 %), loss alone, bf16 4096 x
+// 131072 6430 (95 %), backward pass bf16 4096 x 131072 6400 (94 %).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -118,12 +116,12 @@ __device__ __forceinline__ Split split(float s) {
 struct Sum {
   float m, s;
 };
-// The sum over the first kLanes lanes of a warp (a power of two), on every one of them.
+// The sum over groups of kLanes lanes of a warp (a power of two; every group has the same), on
+// every lane.
 template <int kLanes>
 __device__ __forceinline__ Sum lanes_join(Sum a, float c) {
-  float m = a.m;
-#pragma unroll
-  for (int o = kLanes / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(a.m));
   float s = m == -INFINITY ? a.s : a.s * ex2((a.m - m) * c);
 #pragma unroll
   for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -178,79 +176,121 @@ struct List {
   float* t;
   float* z;    // the student's logit there
   float* p;    // softmax over the list (0 where absent)
-  float* dz;   // the column's gradient
+  float* dz;   // the column's gradient (list_grad())
   __device__ List(unsigned char* base, int kpad)
       : idx(reinterpret_cast<int*>(base)),
         t(reinterpret_cast<float*>(base) + kpad),
         z(reinterpret_cast<float*>(base) + 2 * kpad),
         p(reinterpret_cast<float*>(base) + 3 * kpad),
         dz(reinterpret_cast<float*>(base) + 4 * kpad) {}
-  // By one warp: whether a column may occur twice (lists of up to 64 are looked through).
-  __device__ bool twice(int kpad, int lane) const {
-    if (kpad > 64) return true;
-    const int i0 = lane < kpad ? idx[lane] : -1, i1 = 32 + lane < kpad ? idx[32 + lane] : -1;
-    const uint32_t self = 1u << lane;
-    bool found = __match_any_sync(0xffffffffu, i0) != self && i0 >= 0;
-    if (kpad > 32) {
-      found |= (__match_any_sync(0xffffffffu, i1) != self && i1 >= 0);
-#pragma unroll 8
-      for (int l = 0; l < 32; ++l) {
-        const int other = __shfl_sync(0xffffffffu, i1, l);
-        found |= other == i0 && i0 >= 0;
+  // By one warp: whether a column occurs twice among the first n, through a table of 2 n columns'
+  // hashes in t's place.
+  __device__ bool twice(int n, int lane) const {
+    constexpr unsigned short kNone = 0xffff;
+    unsigned short* seen = reinterpret_cast<unsigned short*>(t);
+    for (int j = lane; j < 2 * n; j += 32) seen[j] = kNone;
+    __syncwarp();
+    bool found = false;
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      const int j = j0 + lane, at = j < n ? idx[j] : -1;
+      uint32_t slot = __umulhi((uint32_t)at * 0x9E3779B1u, 2u * n);
+      for (bool open = at >= 0; __any_sync(0xffffffffu, open);) {
+        if (!open) continue;
+        const unsigned short other = atomicCAS(seen + slot, kNone, (unsigned short)j);
+        if (other == kNone)
+          open = false;
+        else if (idx[other] == at)
+          found = true, open = false;
+        else if (++slot == 2u * n)
+          slot = 0;
       }
     }
     return __any_sync(0xffffffffu, found);
   }
 };
-constexpr int kListBytes = 20;  // per entry
+constexpr int kListBytes = 16;      // per entry
+constexpr int kGradListBytes = 20;  // with dz
 
-// One warp's loader of lists.  begin() asks for a row's first 64 entries, end() (some time later)
-// for the rest and for the student's logits there, and forms p.
-template <typename E>
+// One warp's loader of lists, whose loads from memory take as long as a few units of work: begin()
+// asks for a row's first 64 entries, ask() (some time later) for the student's logits there, end()
+// (later again) puts the list together and loads the rest of a longer one, kBatch * 32 at a time.
+template <typename E, int kBatch = 4>
 struct ListLoader {
-  int64_t i[2];
-  float t[2];
+  int64_t raw[2];  // what begin() asked for
+  float raw_t[2];
+  int at[2];       // what ask() made of it
+  float t[2], z[2];
   __device__ void begin(const DistillArgs& a, int64_t b, int lane) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = h * 32 + lane;
-      i[h] = -1, t[h] = -INFINITY;
-      if (j < a.k) i[h] = a.idx[b * a.k + j], t[h] = a.teacher[b * a.k + j];
+      raw[h] = -1, raw_t[h] = -INFINITY;
+      if (j < a.k) raw[h] = a.idx[b * a.k + j], raw_t[h] = a.teacher[b * a.k + j];
     }
   }
-  // Returns the largest t (-inf for an empty list) and the sum of exp((t - largest) / T).
-  __device__ Sum end(const List& l, const DistillArgs& a, int64_t b, float c, int lane,
-                     bool report) {
-    const E* row = static_cast<const E*>(a.z) + b * a.ld;
+  // The column, -1 if the entry is absent, and the student's logit there; only in this slice unless
+  // `all`, 0 elsewhere.
+  __device__ static int column(const DistillArgs& a, int64_t i, float t, bool report) {
+    if (i >= a.V && report) atomicExch(a.status, PKM_ERR_BAD_INDEX);
+    return i >= 0 && i < a.V && t != -INFINITY ? (int)i : -1;
+  }
+  __device__ static float logit(const Row<E>& row, int slice, bool all, int at) {
+    return at >= 0 && (all || row.mine(at, slice)) ? El<E>::get(row.z[at]) : 0.0f;
+  }
+  __device__ void ask(const DistillArgs& a, const Row<E>& row, int slice, bool all, bool report) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      at[h] = column(a, raw[h], raw_t[h], report), t[h] = raw_t[h];
+      z[h] = logit(row, slice, all, at[h]);
+    }
+  }
+  // Forms p; returns the largest t (-inf for an empty list) and the sum of exp((t - largest) / T).
+  __device__ Sum end(const List& l, const DistillArgs& a, int64_t b, int slice, int lsh, bool all,
+                     bool report, float c, int lane) {
     float tm = -INFINITY;
-    auto entry = [&](int j, int64_t ij, float tj) {
+    auto entry = [&](int j, int aj, float tj, float zj) {
       if (j >= a.kpad) return;
-      if (ij >= a.V && report) atomicExch(a.status, PKM_ERR_BAD_INDEX);
-      const bool there = ij >= 0 && ij < a.V && tj != -INFINITY;
-      l.idx[j] = there ? (int)ij : -1;
-      l.t[j] = tj;
-      l.z[j] = there ? El<E>::get(row[ij]) : 0.0f;
-      if (there) tm = tj > tm || isnan(tj) ? tj : tm;
+      l.idx[j] = aj, l.t[j] = tj, l.z[j] = zj;
+      if (aj >= 0) tm = tj > tm || isnan(tj) ? tj : tm;
     };
-    entry(lane, i[0], t[0]);
-    entry(32 + lane, i[1], t[1]);
-    for (int j = 64 + lane; j < a.kpad; j += 32)
-      entry(j, j < a.k ? a.idx[b * a.k + j] : -1, j < a.k ? a.teacher[b * a.k + j] : -INFINITY);
+    entry(lane, at[0], t[0], z[0]);
+    entry(32 + lane, at[1], t[1], z[1]);
+    if (a.kpad > 64) {
+      const Row<E> row(a, b, slice, lsh, 0);
+      for (int j0 = 64; j0 < a.kpad; j0 += 32 * kBatch) {
+        int64_t i[kBatch];
+        float tj[kBatch], zj[kBatch];
+#pragma unroll
+        for (int h = 0; h < kBatch; ++h) {
+          const int j = j0 + 32 * h + lane;
+          i[h] = -1, tj[h] = -INFINITY;
+          if (j < a.k) i[h] = a.idx[b * a.k + j], tj[h] = a.teacher[b * a.k + j];
+        }
+#pragma unroll
+        for (int h = 0; h < kBatch; ++h) {
+          i[h] = column(a, i[h], tj[h], report);
+          zj[h] = logit(row, slice, all, (int)i[h]);
+        }
+#pragma unroll
+        for (int h = 0; h < kBatch; ++h) entry(j0 + 32 * h + lane, (int)i[h], tj[h], zj[h]);
+      }
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       const float v = __shfl_xor_sync(0xffffffffu, tm, o);
       tm = v > tm || isnan(v) ? v : tm;
     }
-    float total = 0.0f;
-    for (int j = lane; j < a.kpad; j += 32) {
-      const float e = l.idx[j] >= 0 ? ex2((l.t[j] - tm) * c) : 0.0f;
-      l.p[j] = e;
-      total += e;
-    }
+    auto term = [&](int aj, float tj) { return aj >= 0 ? ex2((tj - tm) * c) : 0.0f; };
+    const float e0 = term(at[0], t[0]), e1 = term(at[1], t[1]);
+    float total = e0 + e1;
+    for (int j = 64 + lane; j < a.kpad; j += 32) total += l.p[j] = term(l.idx[j], l.t[j]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     const float inv = total > 0.0f || isnan(total) ? 1.0f / total : 0.0f;
-    for (int j = lane; j < a.kpad; j += 32) l.p[j] *= inv;
+    if (lane < a.kpad) l.p[lane] = e0 * inv;
+    if (32 + lane < a.kpad) l.p[32 + lane] = e1 * inv;
+    for (int j = 64 + lane; j < a.kpad; j += 32) l.p[j] *= inv;
+    __syncwarp();
     return Sum{tm, total};
   }
 };
@@ -294,6 +334,7 @@ __device__ void put_loss(const DistillArgs& a, int64_t b, const Sum& sum, const 
 struct Grad {
   float c, ref, scale, scale_fast, off, off_all;
   bool far;
+  Grad() = default;
   __device__ Grad(float c, float ref, float scale) : c(c), ref(ref), scale(scale) {
     off = -ref * c;
     far = !(fabsf(off) < 1e37f);
@@ -330,13 +371,18 @@ struct GradLse {
   __device__ float fast(float z) const { return ex2(fmaf(z, c, off)) * scale; }
 };
 
-// By `threads` threads (whole warps): the gradients of the listed columns, from z as it was (dz
-// may be z).  Four threads to an entry share the search for others that name its column.
-template <typename G>
-__device__ __forceinline__ void list_grad(const List& list, const DistillArgs& a, const G& q,
-                                          float g, int tid, int threads) {
+// By kThreads threads (whole warps): the gradients of the listed columns, from z as it was (dz may be
+// z).  sum: a column may be there twice; four threads to an entry share the search for its others.
+template <int kThreads, typename G>
+__device__ __forceinline__ void list_grad(const List& list, const DistillArgs& a, bool sum,
+                                          const G& q, float g, int tid) {
+  if (!sum) {
+    for (int j = tid; j < a.k; j += kThreads)
+      if (list.idx[j] >= 0) list.dz[j] = fmaf(-g, list.p[j], q(list.z[j]));
+    return;
+  }
   const int part = tid & 3;
-  for (int j0 = 0; j0 < a.kpad; j0 += threads / 4) {
+  for (int j0 = 0; j0 < a.kpad; j0 += kThreads / 4) {
     const int j = j0 + (tid >> 2);
     if (j0 + ((tid & ~31) >> 2) >= a.kpad) break;  // (a whole warp)
     const int at = j < a.kpad ? list.idx[j] : -1;
@@ -351,6 +397,43 @@ __device__ __forceinline__ void list_grad(const List& list, const DistillArgs& a
     p += __shfl_xor_sync(0xffffffffu, p, 1);
     p += __shfl_xor_sync(0xffffffffu, p, 2);
     if (at >= 0 && part == 0) list.dz[j] = fmaf(-g, p, q(list.z[j]));
+  }
+}
+
+// By one warp: the listed columns of a row's slice, whose values replace those that the row's q alone
+// gave them (z as it was is in the list: dz may be z).  The list is used up: the slice's entries
+// move to its front.
+template <typename E, typename G>
+__device__ __forceinline__ void put_listed(const DistillArgs& a, const Row<E>& row, int slice,
+                                           E* out, const List& list, const G& q, float g,
+                                           int lane) {
+  int n = 0;
+  for (int j0 = 0; j0 < a.kpad; j0 += 32) {
+    const int j = j0 + lane;
+    const int at = j < a.kpad ? list.idx[j] : -1;
+    const bool mine = at >= 0 && row.mine(at, slice);
+    const float p = mine ? list.p[j] : 0.0f, z = mine ? list.z[j] : 0.0f;
+    const uint32_t all = __ballot_sync(0xffffffffu, mine);  // (every lane has read)
+    const int to = n + __popc(all & ((1u << lane) - 1u));
+    if (mine) list.idx[to] = at, list.p[to] = p, list.z[to] = z;
+    n += __popc(all);
+  }
+  if (n + lane < (n + 3) / 4 * 4) list.idx[n + lane] = -1, list.p[n + lane] = 0.0f;
+  __syncwarp();
+  // A column's entries are summed.  More than 64 are looked through for one that occurs twice first:
+  // every entry against every other takes n^2 / 128 steps of the warp.
+  const bool sum = n <= 64 || list.twice(n, lane);
+  for (int j = lane; j < n; j += 32) {
+    const int at = list.idx[j];
+    float p = sum ? 0.0f : list.p[j];
+    if (sum)
+      for (int l = 0; l < n; l += 4) {
+        const int4 i4 = *reinterpret_cast<const int4*>(list.idx + l);
+        const float4 p4 = *reinterpret_cast<const float4*>(list.p + l);
+        p += (i4.x == at ? p4.x : 0.0f) + (i4.y == at ? p4.y : 0.0f) +
+             (i4.z == at ? p4.z : 0.0f) + (i4.w == at ? p4.w : 0.0f);
+      }
+    El<E>::put(out + at, fmaf(-g, p, q(list.z[j])));
   }
 }
 
@@ -502,10 +585,11 @@ distill_warp_kernel(const DistillArgs a) {
   const List list(smem + (size_t)warp * kListBytes * a.kpad, a.kpad);
   const int64_t step = (int64_t)gridDim.x * DWARPS;
   int64_t b = (int64_t)blockIdx.x * DWARPS + warp;
-  ListLoader<E> loader;
+  ListLoader<E, 1> loader;
   if (b < a.B) loader.begin(a, b, lane);
   for (; b < a.B; b += step) {
     const Row<E> row(a, b, 0, 0, lane);
+    loader.ask(a, row, 0, true, true);
     uint4 d[kNV];
 #pragma unroll
     for (int j = 0; j < kNV; ++j)
@@ -513,7 +597,7 @@ distill_warp_kernel(const DistillArgs a) {
     const float x = row.extra >= 0 ? El<E>::get(row.z[row.extra]) : -INFINITY;
     const float g = kMode == kFwd ? 0.0f : a.dloss[b] * a.T;
     const float lse = kMode == kBwd ? a.lse[b] : 0.0f;
-    const Sum ls = loader.end(list, a, b, c, lane, true);
+    const Sum ls = loader.end(list, a, b, 0, 0, true, true, c, lane);
     if (b + step < a.B) loader.begin(a, b + step, lane);
     Sum sum{-INFINITY, 0.0f};
     if constexpr (kMode != kBwd) {
@@ -529,7 +613,6 @@ distill_warp_kernel(const DistillArgs a) {
         if constexpr (kMode == kBwd) return GradLse(lse, g, c);
         else return grad_of(sum, g, c);
       }();
-      if (!zero) list_grad(list, a, q, g, lane, 32);
       E* out = static_cast<E*>(a.dz) + b * a.ld_d;
       const int shift = shift_of(out + row.head);
 #pragma unroll
@@ -541,10 +624,8 @@ distill_warp_kernel(const DistillArgs a) {
           put_vector<E, kSlow>(out + row.head, v, row.nvec, d[j], q, shift, lane);
       }
       if (row.extra >= 0) El<E>::put(out + row.extra, zero ? 0.0f : q(x));
-      __syncwarp();  // the listed columns' values replace those of the row
-      if (!zero)
-        for (int j = lane; j < a.k; j += 32)
-          if (list.idx[j] >= 0) El<E>::put(out + list.idx[j], list.dz[j]);
+      __syncwarp();  // the listed columns come after the row
+      if (!zero) put_listed(a, row, 0, out, list, q, g, lane);
     }
     __syncwarp();
   }
@@ -561,18 +642,22 @@ __global__ void __launch_bounds__(DTHREADS + 32, 3)
 distill_backward_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ Sum s_ls[2];
+  __shared__ bool s_sum[2];  // a column may occur twice in the list
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float c = kLog2e / a.T;
   const int64_t units = (int64_t)a.B << a.lsh;
-  auto list_at = [&](int i) { return List(smem + (size_t)i * kListBytes * a.kpad, a.kpad); };
+  auto list_at = [&](int i) { return List(smem + (size_t)i * kGradListBytes * a.kpad, a.kpad); };
   auto slice_of = [&](int64_t unit) { return (int)(unit & ((1 << a.lsh) - 1)); };
   if (warp == DWARPS) {
     ListLoader<E> loader;
     loader.begin(a, blockIdx.x >> a.lsh, lane);
     int par = 0;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, par ^= 1) {
-      const Sum ls = loader.end(list_at(par), a, unit >> a.lsh, c, lane, slice_of(unit) == 0);
-      if (lane == 0) s_ls[par] = ls;
+      const bool report = slice_of(unit) == 0;
+      loader.ask(a, Row<E>(a, unit >> a.lsh, 0, 0, 0), 0, true, report);
+      const Sum ls = loader.end(list_at(par), a, unit >> a.lsh, 0, 0, true, report, c, lane);
+      const bool sum = a.kpad <= 64 || list_at(par).twice(a.kpad, lane);
+      if (lane == 0) s_ls[par] = ls, s_sum[par] = sum;
       if (unit + gridDim.x < units) loader.begin(a, (unit + gridDim.x) >> a.lsh, lane);
       __syncthreads();
     }
@@ -595,7 +680,7 @@ distill_backward_kernel(const DistillArgs a) {
     __syncthreads();  // the unit's list
     const List list = list_at(par);
     const bool zero = g == 0.0f || s_ls[par].m == -INFINITY;
-    if (!zero) list_grad(list, a, q, g, tid, DTHREADS);
+    if (!zero) list_grad<DTHREADS>(list, a, s_sum[par], q, g, tid);
     E* out = static_cast<E*>(a.dz) + b * a.ld_d;
     const int shift = shift_of(out + row.head);
     auto put = [&](auto form) {
@@ -627,25 +712,33 @@ distill_backward_kernel(const DistillArgs a) {
 //   data warps  each chunk of the slice: maximum and sum (first pass); then (kTrain) each chunk
 //               again: the gradient, written out (second pass).  A vector is always the same
 //               warp's, so the warps need no barrier among themselves;
-//   list warps  (every other row each) join the data warps' sums and send them to the cluster's
-//               CTAs (st.async to shared memory), the rows' lists, the loss (by the slices in
-//               turn);
+//   list warps  (a row each in turn) join the data warps' sums and send them to the cluster's CTAs
+//               (st.async to shared memory), form what the second pass needs from what comes back,
+//               and do the rows' lists: p, the listed columns, the loss (by the slices in turn);
 //   copy warp   the slices' chunks by bulk copies into a ring of slots.
+// The data warps have 8 vectors each of a 32 KB slice, in which every instruction per row counts:
+// with the sums' joining, the gradient's constants and the lists among their work, 4096 x 131072
+// bf16 took 396 us with lists of 64 and 369 with lists of 4, without it 343 and 334.  The lists take a
+// warp longer than the data warps need for a row: two list warps 397 us, three 342, four 344 (and
+// fewer registers).
 // A row's second pass comes after the next row's first, so the exchange costs no waiting, and
 // in kTrain a slot is free when its gradient is written: the ring holds up to three rows'
 // slices, one in each pass and one on its way.
 //
-// Order.  A data warp: first pass of i + 1, local(i + 1), wait sums(i), second pass of i.  A list
-// warp: list i, wait local(i), send i, list i + 2, wait sums(i), loss of i.  local(i): every data
-// warp's sum of row i is written; sums(i): every slice's sum of row i has come.  So
-// - local(i + 2) says that row i's second pass is over (here), sums(i + 2) that it is over or
-//   does not wait for anything of this CTA (elsewhere);
+// Order (kTrain).  A data warp: first pass of i + 1, local(i + 1), wait grad(i), second pass of i.
+// A list warp, for every L-th row (L list warps): wait local(i), send i, wait sums(i), grad(i), the
+// listed columns of i - L, list i + L, loss of i.  local(i): every data warp's sum of row i is
+// written; sums(i): every slice's sum of row i has come; grad(i): what the second pass of i needs is
+// there.  So
+// - local(i + L) says that row i's second pass is over: its listed columns replace what that wrote,
+//   after which its list may go (local(count) and later ones are for these alone);
 // - dz may be z: row i is written after sums(i), so after every CTA has read list i;
-// - list i + 4 is loaded after local(i + 2), a warp's sum i + 4 is written after sums(i + 2), and
-//   another CTA sends i + 4 after its second pass of i + 2, for which this CTA sent i + 2 after
-//   its loss of i: four copies of each do.  In kFwd, without second passes, data warps wait for
-//   sums(i - 3) before they write their sum i, and list warps for sums(i - 2) before they send.
-constexpr int kCopies = 4;
+// - with 2 L copies, a warp's sum i + 2 L is written after grad(i + L), and another CTA sends
+//   i + 2 L after its grad(i + L), for which this CTA has sent i + L: both come after all that
+//   the list warp of row i does for it but its listed columns, which need its own copies only.
+// In kFwd, without second passes, data warps wait for sums(i - L) before they write their sum i.
+constexpr int kListWarps = 3;
+constexpr int kCopies = 2 * kListWarps;
 constexpr int kMaxSlots = 16;
 constexpr int kChunkVecs = 2048;        // 32 KB
 constexpr size_t kDynamic = 216 * 1024;  // dynamic shared memory at most
@@ -665,7 +758,14 @@ struct Geo {
   int shift;  // elements from dz's body to the next 16-byte boundary
 };
 
-constexpr int kData = DWARPS, kListWarps = 2;
+// What the second pass needs of a row, by its list warp.
+struct RowGrad {
+  Grad q;
+  float g;    // dloss * T
+  bool zero;  // no gradient, whatever z holds
+};
+
+constexpr int kData = DWARPS;
 constexpr int kStreamThreads = 32 * (kData + kListWarps + 1);
 template <typename E, int kMode>
 __global__ void __launch_bounds__(kStreamThreads, 3)
@@ -675,12 +775,12 @@ distill_stream_kernel(const DistillArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Sum s_warp[kCopies][kData];
   __shared__ __align__(8) Sum s_slice[kCopies][kMaxSlices];
-  __shared__ float s_tm[kCopies];   // largest t of the list, -inf if it is empty
-  __shared__ int s_twice[kCopies];  // a column may occur twice in the list
+  __shared__ __align__(16) RowGrad s_grad[kCopies];
   __shared__ __align__(16) Geo<E> s_geo[kCopies];
-  __shared__ __align__(8) uint64_t s_bars[2 * kMaxSlots + 2 * kCopies];
+  __shared__ __align__(8) uint64_t s_bars[2 * kMaxSlots + 3 * kCopies];
   __shared__ int s_abort;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = (int)threadIdx.x - 32 * (kListWarps + 1);  // of the data threads
+  const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) - (kListWarps + 1);
   const float c = kLog2e / a.T;
   const int lsh = a.lsh, slices = 1 << lsh;
   const int slots = a.slots, chunk = a.chunk;
@@ -692,7 +792,8 @@ distill_stream_kernel(const DistillArgs a) {
   auto bar_empty = [&](int s) { return bar0 + 8u * (kMaxSlots + s); };
   auto bar_sums = [&](int i) { return bar0 + 8u * (2 * kMaxSlots + i % kCopies); };
   auto bar_local = [&](int i) { return bar0 + 8u * (2 * kMaxSlots + kCopies + i % kCopies); };
-  if (tid == 0) {
+  auto bar_grad = [&](int i) { return bar0 + 8u * (2 * kMaxSlots + 2 * kCopies + i % kCopies); };
+  if (threadIdx.x == 0) {
     for (int s = 0; s < slots; ++s) {
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), kData);
@@ -700,6 +801,7 @@ distill_stream_kernel(const DistillArgs a) {
     for (int i = 0; i < kCopies; ++i) {
       mbar_init(bar_sums(i), 1);
       mbar_init(bar_local(i), kData);
+      mbar_init(bar_grad(i), 1);
     }
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -714,7 +816,7 @@ distill_stream_kernel(const DistillArgs a) {
   const int64_t first = blockIdx.x >> lsh, every = gridDim.x >> lsh;
   const int count = (int)((a.B - first + every - 1) / every);
   auto row_at = [&](int i) { return first + i * every; };
-  if (warp == kData + kListWarps) {
+  if (warp == -1) {
     // ---------------------------------------------------------------- copies
     if (lane == 0) {
       int s = 0, issued = 0;
@@ -767,50 +869,73 @@ distill_stream_kernel(const DistillArgs a) {
                                       ? s_slice[i % kCopies][lane % kMaxSlices]
                                       : Sum{-INFINITY, 0.0f}, c);
   };
-  if (warp >= kData) {
+  if (warp < 0) {
     // ---------------------------------------------------------------- lists, sums, losses
     auto my_loss = [&](int i) { return (i / kListWarps & (slices - 1)) == slice; };
     // (kFwd needs a row's list for its loss alone)
     auto wanted = [&](int i) { return i < count && (kMode == kTrain || my_loss(i)); };
     ListLoader<E> loader;
     Sum ls_next{-INFINITY, 0.0f};
-    auto load = [&](int i) {  // the list asked for before; asks for the one after it
+    auto ask = [&](int i) {  // for its logits, and for the next one's list
       if (wanted(i)) {
-        ls_next = loader.end(list_at(i % kCopies), a, row_at(i), c, lane, my_loss(i));
-        if (kMode == kTrain) {
-          const bool twice = list_at(i % kCopies).twice(a.kpad, lane);
-          if (lane == 0) s_tm[i % kCopies] = ls_next.m, s_twice[i % kCopies] = twice;
-        }
+        const Row<E> row(a, row_at(i), slice, lsh, 0);
+        loader.ask(a, row, slice, my_loss(i), my_loss(i));
       }
-      __syncwarp();
       if (wanted(i + kListWarps)) loader.begin(a, row_at(i + kListWarps), lane);
     };
-    const int h = warp - kData;
+    auto load = [&](int i) {  // what was asked for
+      if (wanted(i))
+        ls_next = loader.end(list_at(i % kCopies), a, row_at(i), slice, lsh, my_loss(i),
+                             my_loss(i), c, lane);
+      ask(i + kListWarps);
+    };
+    const int h = warp + kListWarps + 1;
     if (wanted(h)) loader.begin(a, row_at(h), lane);
+    ask(h);
     load(h);
-    for (int i = h; i < count; i += kListWarps) {
+    // (kTrain: as many rows more, for the listed columns of the last)
+    for (int i = h; i < count + (kMode == kTrain ? kListWarps : 0); i += kListWarps) {
       const Sum ls = ls_next;
-      if (kMode == kFwd && i > 1) wait_sums(i - 2);
       wait_phase(bar_local(i), (uint32_t)(i / kCopies) & 1u, ctl);
       __syncwarp();
-      const Sum sum = lanes_join<kData>(s_warp[i % kCopies][lane & (kData - 1)], c);
-      // to every CTA of the cluster (this one too), completing on the receiver's barrier
-      if (lane == 0) mbar_expect_tx(bar_sums(i), 8u * slices);
-      if (lane < slices)
-        asm volatile(
-            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
-                "r"(mapa_shared(smem_u32(&s_slice[i % kCopies][slice]), lane)),
-            "r"(__float_as_uint(sum.m)), "r"(__float_as_uint(sum.s)),
-            "r"(mapa_shared(bar_sums(i), lane))
-            : "memory");
+      if (i < count) {
+        const Sum sum = lanes_join<kData>(s_warp[i % kCopies][lane & (kData - 1)], c);
+        // to every CTA of the cluster (this one too), completing on the receiver's barrier
+        if (lane == 0) mbar_expect_tx(bar_sums(i), 8u * slices);
+        if (lane < slices)
+          asm volatile(
+              "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::
+                  "r"(mapa_shared(smem_u32(&s_slice[i % kCopies][slice]), lane)),
+              "r"(__float_as_uint(sum.m)), "r"(__float_as_uint(sum.s)),
+              "r"(mapa_shared(bar_sums(i), lane))
+              : "memory");
+      }
+      if (kMode == kTrain && i < count) {
+        const float g = s_geo[i % kCopies].g;
+        wait_sums(i);
+        const Grad q = grad_of(sum_of(i), g, c);
+        if (lane == 0) {
+          s_grad[i % kCopies] = RowGrad{q, g, g == 0.0f || ls.m == -INFINITY};
+          mbar_arrive(bar_grad(i));
+        }
+      }
+      // an earlier row is written but for its listed columns
+      if (kMode == kTrain && i >= kListWarps && !s_grad[(i - kListWarps) % kCopies].zero) {
+        const RowGrad last = s_grad[(i - kListWarps) % kCopies];
+        const int64_t b = row_at(i - kListWarps);
+        const List list = list_at((i - kListWarps) % kCopies);
+        put_listed(a, Row<E>(a, b, slice, lsh, 0), slice, static_cast<E*>(a.dz) + b * a.ld_d, list,
+                   last.q, last.g, lane);
+      }
+      __syncwarp();
       load(i + kListWarps);
-      if (my_loss(i)) {
+      if (i < count && my_loss(i)) {
         wait_sums(i);
         put_loss(a, row_at(i), sum_of(i), list_at(i % kCopies), ls, lane);
       }
     }
     // the other CTAs' last sums are here before this CTA's memory goes
-    for (int i = max(0, count - 2); i < count; ++i) wait_sums(i);
+    for (int i = max(0, count - kListWarps); i < count; ++i) wait_sums(i);
     return;
   }
   // ------------------------------------------------------------------ data
@@ -821,7 +946,7 @@ distill_stream_kernel(const DistillArgs a) {
     x_last = x;
     if (i < count) {
       Sum sum{-INFINITY, 0.0f};
-      wait_phase(bar_full(s1), ph, ctl);
+      if (!__all_sync(0xffffffffu, wait_phase(bar_full(s1), ph, ctl))) return;  // (gave up)
       const Geo<E>& geo = s_geo[i % kCopies];
       const int total = geo.n;
       x = -INFINITY;
@@ -840,19 +965,20 @@ distill_stream_kernel(const DistillArgs a) {
       }
       if (geo.ends) add_one(sum, x, c);
       sum = lanes_join<32>(sum, c);
-      if (kMode == kFwd && i > 2) wait_sums(i - 3);
+      if (kMode == kFwd && i >= kListWarps) wait_sums(i - kListWarps);
       if (lane == 0) {
         s_warp[i % kCopies][warp] = sum;
         mbar_arrive(bar_local(i));
       }
+    } else if (kMode == kTrain && lane == 0) {
+      mbar_arrive(bar_local(i));
     }
     if (kMode == kTrain && i > 0) {
       const Geo<E>& geo = s_geo[(i - 1) % kCopies];
-      const List list = list_at((i - 1) % kCopies);
-      const float g = geo.g;
-      wait_sums(i - 1);
-      const bool zero = g == 0.0f || s_tm[(i - 1) % kCopies] == -INFINITY;  // whatever z holds
-      const Grad q = grad_of(sum_of(i - 1), g, c);
+      wait_phase(bar_grad(i - 1), (uint32_t)((i - 1) / kCopies) & 1u, ctl);
+      __syncwarp();
+      const bool zero = s_grad[(i - 1) % kCopies].zero;
+      const Grad q = s_grad[(i - 1) % kCopies].q;
       E* body = geo.body;
       const int total = geo.n;
       const int shift = geo.shift;
@@ -885,34 +1011,10 @@ distill_stream_kernel(const DistillArgs a) {
       E* out = body - ((int64_t)geo.v0 * kPer + geo.head);
       if (tid < geo.ends)
         El<E>::put(out + (tid < geo.head ? tid : geo.nvec * kPer + tid), zero ? 0.0f : q(x_last));
-      // this warp's listed columns: their values replace those of the row
-      __syncwarp();
-      if (!zero) {
-        const bool twice = s_twice[(i - 1) % kCopies];
-        for (int j0 = 0; j0 < a.k; j0 += 32) {
-          const int j = j0 + lane;
-          const int at = j < a.k ? list.idx[j] : -1;
-          const int v = (at - geo.head) / kPer - geo.v0;
-          const bool outside = at < geo.head || at >= geo.head + geo.nvec * kPer;
-          const bool mine =
-              at >= 0 && (outside ? slice == 0 && warp == 0
-                                  : v >= 0 && v < total && (v & (kThreads - 1)) >> 5 == warp);
-          float p = mine ? list.p[j] : 0.0f;
-          if (twice && __any_sync(0xffffffffu, mine)) {
-            p = 0.0f;  // of every entry that names the column
-            if (mine)
-              for (int l = 0; l < a.kpad; l += 4) {
-                const int4 i4 = *reinterpret_cast<const int4*>(list.idx + l);
-                const float4 p4 = *reinterpret_cast<const float4*>(list.p + l);
-                p += (i4.x == at ? p4.x : 0.0f) + (i4.y == at ? p4.y : 0.0f) +
-                     (i4.z == at ? p4.z : 0.0f) + (i4.w == at ? p4.w : 0.0f);
-              }
-          }
-          if (mine) El<E>::put(out + at, fmaf(-g, p, q(list.z[j])));
-        }
-      }
     }
   }
+  if (kMode == kTrain && lane == 0)
+    for (int i = 1; i < kListWarps; ++i) mbar_arrive(bar_local(count + i));
 }
 
 // CTAs that run at one time at most, for a grid that leaves no second round to a few.
@@ -945,11 +1047,11 @@ cudaError_t launch_backward(DistillArgs& a, cudaStream_t stream) {
   static int most = 0;
   auto kernel = distill_backward_kernel<E>;
   cudaError_t e =
-      resident_ctas(&most, kernel, DTHREADS + 32, (size_t)2 * PKM_DISTILL_MAX_K * kListBytes);
+      resident_ctas(&most, kernel, DTHREADS + 32, (size_t)2 * PKM_DISTILL_MAX_K * kGradListBytes);
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)a.B << a.lsh;
   kernel<<<(unsigned)(units < most ? units : most), DTHREADS + 32,
-           (size_t)2 * kListBytes * a.kpad, stream>>>(a);
+           (size_t)2 * kGradListBytes * a.kpad, stream>>>(a);
   return cudaGetLastError();
 }
 
