@@ -22,11 +22,12 @@
 //
 // Bound by the tensor pipe in long products: 92 to 95 % busy in the gate and in the backward
 // pass's last four at 4096 x 2048 x 8192, 81 % in the down projection (128 tiles on 74 clusters),
-// at the clock that 1400 W leaves.  A tile of 256 x 256 writes and reads shared memory at nearly
-// the rate that it has, so what an epilogue moves through it costs time: the backward gate's
-// (five tensors, 20 KB per 32 x 32 block) leaves the tensor pipe 53 % busy.  Its other forms
-// took longer: g and u through registers 469 us at 16384 x 2048 x 8192, h stored directly 508, this
-// one 432.
+// at the clock that 1400 W leaves.  Each SM takes 180 GB/s of operands from L2 then, about what L2
+// gives all of them, so what an epilogue moves beside them costs time: the backward gate (five
+// tensors through it) takes 424 us at 16384 x 2048 x 8192, of which the product alone is 266, the
+// loads of g and u 70 and the stores of dg, du and h 85; its arithmetic is hidden.  g and u through
+// registers took 469 us, h stored directly 508, g and u prefetched into L2 438, asked for two blocks
+// ahead from tile to tile with blocks of their own for the results 433.
 //
 // One launch takes several products (the backward pass's last four), so that
 // small ones fill the GPU together.  Work is split evenly over the clusters
@@ -204,12 +205,6 @@ __device__ __forceinline__ void add_block(const CUtensorMap* map, uint32_t buf, 
       "r"(col), "r"(row), "r"(buf)
       : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-__device__ __forceinline__ void prefetch_block(const CUtensorMap* map, int col, int row) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(col), "r"(row)
-               : "memory");
 }
 // All but the last kPending stores of this thread have read their blocks.
 template <int kPending>
@@ -440,10 +435,6 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       if (kEpi == kDGate && sg.part < 0 && row0 < M && lane == 0) {
         if (cols > 0) ask(0);
         if (cols > 32) ask(32);
-        for (int c = 64; c < cols; c += 32) {  // the others into L2 meanwhile
-          prefetch_block(&p.in[0], col0 + c, row0);
-          prefetch_block(&p.in[1], col0 + c, row0);
-        }
       }
       __syncwarp();
       if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_tfull(buf), use & 1u, ctl))) break;
