@@ -794,7 +794,7 @@ cudaError_t launch_gemm(GemmArgs& p, const BOperand (&b)[kMaxProds][2], cudaStre
 }  // namespace
 
 size_t gated_ffn_workspace_bytes(int B, int F) {
-  return align256((size_t)B * F * 2) + parts_bytes(B);
+  return align256((size_t)B * F * 2) + (B > kFewTokens ? parts_bytes(B) : 0);
 }
 size_t gated_ffn_backward_workspace_bytes(int B, int F) {
   return 3 * align256((size_t)B * F * 2) + parts_bytes(FM);
