@@ -21,7 +21,7 @@
 // 8192 that way, 600 this way).
 //
 // Bound by the tensor pipe in long products: 92 to 95 % busy in the gate and in the backward
-// pass's last four at 4096 x 2048 x 8192, 81 % in the down projection (128 tiles on 74 clusters),
+// pass's last four at 4096 x 2048 x 8192, 81 % in the down projection (128 tiles on 76 clusters),
 // at the clock that 1400 W leaves.  Each SM takes 180 GB/s of operands from L2 then, about what L2
 // gives all of them, so what an epilogue moves beside them costs time: the backward gate (five
 // tensors through it) takes 424 us at 16384 x 2048 x 8192, of which the product alone is 266, the
