@@ -138,14 +138,19 @@ def _addr(x):
     raise TypeError("cannot take the address of %r" % type(x))
 
 
+_current_stream = None
+
+
 def _stream(s):
+    global _current_stream
     if s is None:
-        import torch
-        # (the raw handle alone, where torch offers it: building a Stream object takes 3 us)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            # (the raw handle alone, where torch offers it: building a Stream object takes 3 us)
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _current_stream = ((lambda: raw(device())) if raw is not None else
+                               lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -355,8 +360,10 @@ def pkm_gated_ffn(x, w_gate, w_up, w_down, B, dim, F, act, workspace, y, gate=No
                   status=None, stream=None):
     """y = (act(x w_gate^T) * (x w_up^T)) w_down^T in bf16; gate and up keep the two projections
     for the backward pass (see include/pkm.h)."""
-    a = [_dense(t, "pkm_gated_ffn") for t in (x, w_gate, w_up, w_down, workspace, y, gate, up)]
-    return lib().pkm_gated_ffn(*a[:4], B, dim, F, act, *a[4:], _addr(status), _stream(stream))
+    w = "pkm_gated_ffn"
+    return lib().pkm_gated_ffn(_dense(x, w), _dense(w_gate, w), _dense(w_up, w), _dense(w_down, w),
+                               B, dim, F, act, _dense(workspace, w), _dense(y, w), _dense(gate, w),
+                               _dense(up, w), _addr(status), _stream(stream))
 
 
 def pkm_gated_ffn_backward_workspace_bytes(B, dim, F):

@@ -118,7 +118,7 @@ struct GemmArgs {
   int part_rows;
   unsigned long long* flags;    // [stretch][CTA of the pair][epilogue warp]
   unsigned long long epoch;     // a flag's value when its part is there
-  int* status;
+  int* status;  // may be NULL
 };
 
 // Segment i of cluster c; false past the last.
@@ -286,7 +286,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   tc_fence_after();
   cluster_sync();  // both CTAs' barriers exist before any remote arrival
   const uint32_t tmem = s_tmem_base;
-  const Ctl ctl{&s_abort, p.status};
+  const Ctl ctl{&s_abort, status_of(p.status)};
 
   // A call's later launches begin before the one before them has ended (programmatic dependent
   // launch): everything up to here.
@@ -470,7 +470,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
                 asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(f) : "l"(flag) : "memory");
                 if (f != p.epoch && globaltimer() - begun > WAIT_LIMIT_NS) {
                   s_abort = 1;
-                  atomicExch(p.status, PKM_ERR_TIMEOUT);
+                  atomicExch(status_of(p.status), PKM_ERR_TIMEOUT);
                   break;
                 }
               } while (f != p.epoch && !*ctl.abort);
@@ -897,19 +897,7 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
 
 namespace {
 
-// device status word for calls that pass none
-__device__ int g_ffn_status;
-
 bool ffn_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int ffn_status(int* status, int** out) {
-  *out = status;
-  if (status) return PKM_OK;
-  void* p = nullptr;
-  if (cudaGetSymbolAddress(&p, g_ffn_status) != cudaSuccess) return PKM_ERR_CUDA;
-  *out = static_cast<int*>(p);
-  return PKM_OK;
-}
 
 int ffn_check(int B, int dim, int F, int act) {
   if (B < 0 || dim < 1 || F < 1) return PKM_ERR_INVALID;
@@ -946,9 +934,7 @@ extern "C" int pkm_gated_ffn(const void* x, const void* w_gate, const void* w_up
   for (const void* p : {x, w_gate, w_up, w_down, (const void*)workspace, (const void*)y,
                         (const void*)gate, (const void*)up})
     if (!ffn_aligned16(p)) return PKM_ERR_ALIGN;
-  int* st;
-  if ((rc = ffn_status(status, &st))) return rc;
-  return pkm::launch_gated_ffn(x, w_gate, w_up, w_down, B, dim, F, act, workspace, y, gate, up, st,
+  return pkm::launch_gated_ffn(x, w_gate, w_up, w_down, B, dim, F, act, workspace, y, gate, up, status,
                                static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKM_OK
              : PKM_ERR_CUDA;
@@ -977,10 +963,8 @@ extern "C" int pkm_gated_ffn_backward(const void* x, const void* w_gate, const v
                         (const void*)dx, (const void*)dw_gate, (const void*)dw_up,
                         (const void*)dw_down})
     if (!ffn_aligned16(p)) return PKM_ERR_ALIGN;
-  int* st;
-  if ((rc = ffn_status(status, &st))) return rc;
   return pkm::launch_gated_ffn_backward(x, w_gate, w_up, w_down, gate, up, dy, B, dim, F, act,
-                                        workspace, dx, dw_gate, dw_up, dw_down, grad_dtype, st,
+                                        workspace, dx, dw_gate, dw_up, dw_down, grad_dtype, status,
                                         static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKM_OK
              : PKM_ERR_CUDA;

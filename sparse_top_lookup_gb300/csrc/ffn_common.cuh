@@ -24,6 +24,11 @@ __device__ __forceinline__ float sigmoid2(float x2) { return rcp(1.0f + ex2(-x2)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi): (1 + tanh v) / 2 = sigmoid(2 v)
 
+// What calls without a status word report into (looked up by the kernels: the address costs the
+// host 0.3 us a call).
+static __device__ int g_ffn_status;
+__device__ __forceinline__ int* status_of(int* status) { return status ? status : &g_ffn_status; }
+
 // act(g) and act'(g)
 template <int kAct>
 __device__ __forceinline__ float2 act_both(float g) {

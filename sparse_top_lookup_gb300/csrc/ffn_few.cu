@@ -50,7 +50,7 @@ struct FewArgs {
   int act, keep, dependent;
   __nv_bfloat16 *out0, *out1, *out2;  // [T, M]: kFewGate h, g, u; kFewStore C; kFewDGate dg, du, h
   const __nv_bfloat16 *g_in, *u_in;   // kFewDGate
-  int* status;
+  int* status;  // may be NULL
 };
 
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
@@ -108,7 +108,7 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem_base;
-  const Ctl ctl{&s_abort, p.status};
+  const Ctl ctl{&s_abort, status_of(p.status)};
   if (!p.dependent) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
