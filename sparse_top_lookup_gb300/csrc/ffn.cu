@@ -111,7 +111,6 @@ struct GemmArgs {
   CUtensorMap more[2];  // kGate (out: h): g, u; kDGate (out: dg): du, h
   CUtensorMap in[2];    // kDGate: g, u
   int prods, act, keep;  // keep: kGate writes g and u
-  int dependent;         // on the launch before it
   Plan plan;
   const __nv_bfloat16 *g_in, *u_in;  // kDGate
   float4* parts;                // [stretch][CTA of the pair][column / 4][row], part_rows rows
@@ -288,10 +287,10 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   const uint32_t tmem = s_tmem_base;
   const Ctl ctl{&s_abort, status_of(p.status)};
 
-  // A call's later launches begin before the one before them has ended (programmatic dependent
-  // launch): everything up to here.
+  // Everything up to here may run before the launch before this one has ended (programmatic
+  // dependent launch); no memory is read or written until it has.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // The two issuing warps run their loops with all lanes and elect one only around what it
   // issues: with the loop in one lane's branch a step took 0.22 us more or less whatever it
@@ -740,7 +739,7 @@ cudaError_t launch_tiles(GemmArgs& p, cudaStream_t stream, int* most) {
   cfg.dynamicSmemBytes = Tile<kEpi, kN>::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = p.dependent && !most ? 2 : 1;
+  cfg.numAttrs = most ? 1 : 2;
   if (most) {  // how many clusters run at one time
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Tile<kEpi, kN>::kSmem);
@@ -821,7 +820,6 @@ cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up
   cudaError_t e = launch_gemm<kGate>(p, {{{w_gate, F, dim}, {w_up, F, dim}}}, stream);
   if (e != cudaSuccess) return e;
   q.N = dim, q.K = F;
-  p.dependent = 1;
   if (!operand(&q.a[0], workspace, B, F, false) || !result(&q.out, y, B, dim))
     return cudaErrorInvalidValue;
   return launch_gemm<kStore>(p, {{{w_down, dim, F}}}, stream);
@@ -861,7 +859,6 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
     if (e != cudaSuccess) return e;
   }
   // the rest in one launch
-  p.dependent = 1;
   const bool add = grad_dtype == PKM_F32;
   BOperand b[kMaxProds][2] = {};
   p.prods = 0;

@@ -14,7 +14,7 @@
 // in flight, and the second kernel of a call starts while the first one runs (programmatic
 // dependent launch; both fit on an SM): it fills its ring with weights and waits for the first
 // only before it loads the tokens' rows.  Rings of 64 and 180 KB: 11.4 and 17 us at one token of
-// 1024 x 4096 (captured; this one 12), 31 and 42 at 37 of 2048 x 8192 (this one 28).
+// 1024 x 4096 (captured; this one 12 then, 11 now), 31 and 42 at 37 of 2048 x 8192 (this one 28).
 //
 // Measured at 37 tokens of 2048 x 8192 (100 MB of weights, 14.8 us at the copy's rate): 28 us
 // captured.  The gate's weights stream from 2.4 to 15 us at 5.4 TB/s and its results are out at
@@ -109,7 +109,10 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
   tc_fence_after();
   const uint32_t tmem = s_tmem_base;
   const Ctl ctl{&s_abort, status_of(p.status)};
-  if (!p.dependent) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // A call's first launch may begin, up to here, before the launch before it has ended; its second
+  // begins when all of the first are here, after what came before, so it may read weights.
+  if (!p.dependent) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------ copies
@@ -372,7 +375,7 @@ cudaError_t launch_few(FewArgs& p, const void* w0, const void* w1, const void* t
   cfg.dynamicSmemBytes = bytes + 1024;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = p.dependent ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
