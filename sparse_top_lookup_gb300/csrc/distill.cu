@@ -44,6 +44,13 @@ constexpr int kWarpMaxK = 128;   // longest list of the warp-per-row form (its s
 
 enum Mode { kFwd, kBwd, kTrain };
 
+// Set-up before this may run before the launch before this one has ended (programmatic dependent
+// launch); no memory is read or written until it has.
+__device__ __forceinline__ void after_earlier_work() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <typename E>
 struct El;
 template <>
@@ -624,6 +631,7 @@ distill_warp_kernel(const DistillArgs a) {
   const List list(smem + (size_t)warp * kListBytes * a.kpad, a.kpad);
   const int64_t step = (int64_t)gridDim.x * DWARPS;
   int64_t b = (int64_t)blockIdx.x * DWARPS + warp;
+  after_earlier_work();
   ListLoader<E, 1> loader;
   if (b < a.B) loader.begin(a, b, lane);
   for (; b < a.B; b += step) {
@@ -847,6 +855,7 @@ distill_stream_kernel(const DistillArgs a) {
   }
   __syncthreads();
   cluster_sync();  // every CTA's barriers exist before its memory is written
+  after_earlier_work();
   const Ctl ctl{&s_abort, status_of(a)};
 
   // this CTA's slice (consecutive CTAs, a cluster's, have those of one row) of rows first + i *
@@ -1068,6 +1077,26 @@ cudaError_t resident_ctas(int* out, K kernel, int threads, size_t smem) {
   return cudaSuccess;
 }
 
+struct Launch {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg;
+  Launch(unsigned grid, int threads, size_t smem, int cluster, cudaStream_t stream) : cfg{} {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+  Launch(const Launch&) = delete;
+};
+
 template <typename E, int kNV, int kMode>
 cudaError_t launch_warps(const DistillArgs& a, cudaStream_t stream) {
   static int most = 0;
@@ -1075,8 +1104,9 @@ cudaError_t launch_warps(const DistillArgs& a, cudaStream_t stream) {
   cudaError_t e = resident_ctas(&most, kernel, DTHREADS, (size_t)DWARPS * kWarpMaxK * kListBytes);
   if (e != cudaSuccess) return e;
   const int ctas = (a.B + DWARPS - 1) / DWARPS;
-  kernel<<<ctas < most ? ctas : most, DTHREADS, (size_t)DWARPS * kListBytes * a.kpad, stream>>>(a);
-  return cudaGetLastError();
+  const Launch l(ctas < most ? ctas : most, DTHREADS, (size_t)DWARPS * kListBytes * a.kpad, 1,
+                 stream);
+  return cudaLaunchKernelEx(&l.cfg, kernel, a);
 }
 
 template <typename E>
@@ -1099,17 +1129,7 @@ cudaError_t launch_stream(const DistillArgs& a, cudaStream_t stream) {
   auto kernel = distill_stream_kernel<E, kMode>;
   const int slices = 1 << a.lsh;
   const size_t smem = (size_t)a.slots * a.chunk * 16 + (size_t)kCopies * kListBytes * a.kpad;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = slices;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  Launch l(0, kStreamThreads, smem, slices, stream);
   // clusters that run at one time, by their size and shared memory (in steps of 4 KB)
   constexpr size_t kStep = 4096;
   static int most[kMaxLsh + 1][kDynamic / kStep + 1];
@@ -1123,17 +1143,21 @@ cudaError_t launch_stream(const DistillArgs& a, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
       attr_set = true;
     }
-    cfg.dynamicSmemBytes = step * kStep;
-    cfg.gridDim = dim3(slices * tc::sm_count());
+    Launch most_of(slices * tc::sm_count(), kStreamThreads, step * kStep, slices, stream);
+    most_of.cfg.numAttrs = 1;
     int got = 0;
-    cudaError_t e = cudaOccupancyMaxActiveClusters(&got, kernel, &cfg);
+    cudaError_t e = cudaOccupancyMaxActiveClusters(&got, kernel, &most_of.cfg);
     if (e != cudaSuccess) return e;
     if (got < 1) return cudaErrorInvalidConfiguration;
     n = got;
-    cfg.dynamicSmemBytes = smem;
   }
-  cfg.gridDim = dim3((unsigned)(a.B < n ? a.B : n) * slices);
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  l.cfg.gridDim = dim3((unsigned)(a.B < n ? a.B : n) * slices);
+  // Not before the launch before it has ended where larger clusters fill the GPU: placed as SMs
+  // become free one after the other, fewer of them run at one time (kTrain, a row of calls: 8 slices,
+  // 4096 x 131072 bf16, 381 us against 340; 4 slices, 2000 x 60000, 98 against 95; 2 slices, 4096 x 32000,
+  // 98 against 101; kFwd, 4 slices, 2000 x 50257, 40 against 42).
+  if (kMode == kTrain && slices > 2) l.cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&l.cfg, kernel, a);
 }
 
 template <typename E, int kMode>
