@@ -473,7 +473,7 @@ int pkm_query_net_batch(const void *x, const void *weight, int B, int dim, int F
  * status: as pkm_query_net's.  Errors: PKM_ERR_INVALID (NULL pointer, B < 0,
  * dim < 1, F < 1, one of two that go together), PKM_ERR_UNSUPPORTED (dim or F
  * no multiple of 8, act, grad_dtype), PKM_ERR_RANGE (a product's tiles above
- * 2^31 - 1), PKM_ERR_ALIGN (a pointer not 16-byte aligned), PKM_ERR_CUDA.
+ * 2^31 - 1), PKM_ERR_ALIGN (a pointer not 16-byte aligned; status: 4), PKM_ERR_CUDA.
  */
 enum {
   PKM_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
@@ -518,7 +518,8 @@ int pkm_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up,
  * PKM_DISTILL_MAX_K.  lse is fp32: where a row's logits are all so far from zero
  * (10^5 T and more, as when every one is a mask of a large negative value) that lse cannot hold
  * log V beside them, pkm_distill_backward's q is no better than that, while
- * pkm_distill_train's is exact.
+ * pkm_distill_train's is exact (for V up to 262144 of bf16 or 131072 of fp32; longer rows go through the
+ * other two).
  *
  * pkm_distill: loss, and lse unless NULL.  pkm_distill_backward: dlogits from
  * the forward's lse and the loss's gradient dloss.  pkm_distill_train: all

@@ -1261,8 +1261,16 @@ int distill_check(int dtype, int64_t ld, int B, int V, int k, float T) {
 }
 
 // Pointers to whole elements: what CUDA's own types ask for.
-bool distill_aligned(const void* p, int dtype) {
-  return (reinterpret_cast<uintptr_t>(p) & (dtype == PKM_BF16 ? 1u : 3u)) == 0;
+bool whole(const void* p, uintptr_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+// (those that a call has none of are NULL)
+bool distill_aligned(int dtype, const void* logits, const void* dlogits, const int64_t* idx,
+                     const float* teacher, const float* loss, const float* lse,
+                     const float* dloss, const int* status) {
+  const uintptr_t e = dtype == PKM_BF16 ? 2 : 4;
+  return whole(logits, e) && whole(dlogits, e) && whole(idx, 8) && whole(teacher, 4) &&
+         whole(loss, 4) && whole(lse, 4) && whole(dloss, 4) && whole(status, 4);
 }
 
 }  // namespace
@@ -1273,7 +1281,8 @@ extern "C" int pkm_distill(const void* logits, int logit_dtype, int64_t ld, int 
   int rc = distill_check(logit_dtype, ld, B, V, k, temperature);
   if (rc || B == 0) return rc;
   if (!logits || !idx || !teacher || !loss) return PKM_ERR_INVALID;
-  if (!distill_aligned(logits, logit_dtype)) return PKM_ERR_ALIGN;
+  if (!distill_aligned(logit_dtype, logits, nullptr, idx, teacher, loss, lse, nullptr, status))
+    return PKM_ERR_ALIGN;
   return pkm::launch_distill(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature, loss,
                              lse, status, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKM_OK
@@ -1289,7 +1298,7 @@ extern "C" int pkm_distill_backward(const void* logits, int logit_dtype, int64_t
   if (ld_d < V || (logits == dlogits && ld != ld_d)) return PKM_ERR_RANGE;
   if (B == 0) return PKM_OK;
   if (!logits || !idx || !teacher || !lse || !dloss || !dlogits) return PKM_ERR_INVALID;
-  if (!distill_aligned(logits, logit_dtype) || !distill_aligned(dlogits, logit_dtype))
+  if (!distill_aligned(logit_dtype, logits, dlogits, idx, teacher, nullptr, lse, dloss, status))
     return PKM_ERR_ALIGN;
   return pkm::launch_distill_backward(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature,
                                       lse, dloss, dlogits, ld_d, status,
@@ -1307,7 +1316,7 @@ extern "C" int pkm_distill_train(const void* logits, int logit_dtype, int64_t ld
   if (ld_d < V || (logits == dlogits && ld != ld_d)) return PKM_ERR_RANGE;
   if (B == 0) return PKM_OK;
   if (!logits || !idx || !teacher || !dloss || !loss || !lse || !dlogits) return PKM_ERR_INVALID;
-  if (!distill_aligned(logits, logit_dtype) || !distill_aligned(dlogits, logit_dtype))
+  if (!distill_aligned(logit_dtype, logits, dlogits, idx, teacher, loss, lse, dloss, status))
     return PKM_ERR_ALIGN;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return pkm::launch_distill_train(logits, logit_dtype, ld, B, V, idx, teacher, k, temperature,

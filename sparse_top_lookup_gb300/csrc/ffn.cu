@@ -895,6 +895,7 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
 namespace {
 
 bool ffn_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool ffn_aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int ffn_check(int B, int dim, int F, int act) {
   if (B < 0 || dim < 1 || F < 1) return PKM_ERR_INVALID;
@@ -931,6 +932,7 @@ extern "C" int pkm_gated_ffn(const void* x, const void* w_gate, const void* w_up
   for (const void* p : {x, w_gate, w_up, w_down, (const void*)workspace, (const void*)y,
                         (const void*)gate, (const void*)up})
     if (!ffn_aligned16(p)) return PKM_ERR_ALIGN;
+  if (!ffn_aligned4(status)) return PKM_ERR_ALIGN;
   return pkm::launch_gated_ffn(x, w_gate, w_up, w_down, B, dim, F, act, workspace, y, gate, up, status,
                                static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKM_OK
@@ -960,6 +962,7 @@ extern "C" int pkm_gated_ffn_backward(const void* x, const void* w_gate, const v
                         (const void*)dx, (const void*)dw_gate, (const void*)dw_up,
                         (const void*)dw_down})
     if (!ffn_aligned16(p)) return PKM_ERR_ALIGN;
+  if (!ffn_aligned4(status)) return PKM_ERR_ALIGN;
   return pkm::launch_gated_ffn_backward(x, w_gate, w_up, w_down, gate, up, dy, B, dim, F, act,
                                         workspace, dx, dw_gate, dw_up, dw_down, grad_dtype, status,
                                         static_cast<cudaStream_t>(stream)) == cudaSuccess
