@@ -217,9 +217,10 @@ struct List {
         z(reinterpret_cast<float*>(base) + 2 * kpad),
         p(reinterpret_cast<float*>(base) + 3 * kpad),
         dz(reinterpret_cast<float*>(base) + 4 * kpad) {}
-  // By one warp: whether a column occurs twice among the first n, through a table of 2 n columns'
-  // hashes in t's place.
-  __device__ bool twice(int n, int lane) const {
+  // By one warp: whether a column occurs twice among those of the first n that count(column), through
+  // a table of 2 n columns' hashes in t's place.
+  template <typename F>
+  __device__ bool twice(int n, int lane, F&& count) const {
     constexpr unsigned short kNone = 0xffff;
     unsigned short* seen = reinterpret_cast<unsigned short*>(t);
     for (int j = lane; j < 2 * n; j += 32) seen[j] = kNone;
@@ -228,7 +229,7 @@ struct List {
     for (int j0 = 0; j0 < n; j0 += 32) {
       const int j = j0 + lane, at = j < n ? idx[j] : -1;
       uint32_t slot = __umulhi((uint32_t)at * 0x9E3779B1u, 2u * n);
-      for (bool open = at >= 0; __any_sync(0xffffffffu, open);) {
+      for (bool open = at >= 0 && count(at); __any_sync(0xffffffffu, open);) {
         if (!open) continue;
         const unsigned short other = atomicCAS(seen + slot, kNone, (unsigned short)j);
         if (other == kNone)
@@ -456,7 +457,7 @@ __device__ __forceinline__ void put_listed(const DistillArgs& a, const Row<E>& r
   __syncwarp();
   // A column's entries are summed.  More than 64 are looked through for one that occurs twice first:
   // every entry against every other takes n^2 / 128 steps of the warp.
-  const bool sum = n <= 64 || list.twice(n, lane);
+  const bool sum = n <= 64 || list.twice(n, lane, [](int) { return true; });
   for (int j = lane; j < n; j += 32) {
     const int at = list.idx[j];
     float p = sum ? 0.0f : list.p[j];
@@ -681,8 +682,8 @@ distill_warp_kernel(const DistillArgs a) {
 // kBwd: units of 8 vectors per data thread, each by itself, in registers.  A list warp is a unit
 // ahead with the lists (two copies: a unit's is in use until the next unit's barrier).  lse is
 // known, so nothing is exchanged and units need no ring: loads of 8 vectors per thread and three
-// CTAs per SM cover HBM's latency.  fp32 1500 x 50257 99 us (6090 GB/s, 90 %), bf16 4096 x 131072
-// 370 (5810; lists of 4: 338).
+// CTAs per SM cover HBM's latency.  fp32 1500 x 50257 97 us (6220 GB/s, 92 %), bf16 4096 x 131072
+// with lists of 64 337 (6380), with lists of 4 333.
 constexpr int kBwdVecs = 8;
 template <typename E>
 __global__ void __launch_bounds__(DTHREADS + 32, 3)
@@ -700,10 +701,14 @@ distill_backward_kernel(const DistillArgs a) {
     loader.begin(a, blockIdx.x >> a.lsh, lane);
     int par = 0;
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, par ^= 1) {
-      const bool report = slice_of(unit) == 0;
-      loader.ask(a, Row<E>(a, unit >> a.lsh, 0, 0, 0), 0, true, report);
-      const Sum ls = loader.end(list_at(par), a, unit >> a.lsh, 0, 0, true, report, c, lane);
-      const bool sum = a.kpad <= 64 || list_at(par).twice(a.kpad, lane);
+      const int slice = slice_of(unit);
+      const bool report = slice == 0;
+      const Row<E> row(a, unit >> a.lsh, slice, a.lsh, 0);
+      loader.ask(a, row, slice, false, report);
+      const Sum ls = loader.end(list_at(par), a, unit >> a.lsh, slice, a.lsh, false, report, c, lane);
+      const bool sum = a.kpad <= 64 || list_at(par).twice(a.kpad, lane, [&](int at) {
+        return row.mine(at, slice);
+      });
       if (lane == 0) s_ls[par] = ls, s_sum[par] = sum;
       if (unit + gridDim.x < units) loader.begin(a, (unit + gridDim.x) >> a.lsh, lane);
       __syncthreads();
