@@ -248,8 +248,10 @@ constexpr int kGradListBytes = 20;  // with dz
 
 // One warp's loader of lists, whose loads from memory take as long as a few units of work: begin()
 // asks for a row's first 64 entries, ask() (some time later) for the student's logits there, end()
-// (later again) puts the list together and loads the rest of a longer one, kBatch * 32 at a time.
-template <typename E, int kBatch = 4>
+// (later again) puts the list together and loads the rest of a longer one, kBatch * 32 at a time
+// (more cost registers, which lists of up to 64 pay for too: training step 4096 x 131072 bf16, k = 64 and 128,
+// with 1, 2, 4 and 8: 338 and 421, 340 and 404, 342 and 438, 385 and 527 us).
+template <typename E, int kBatch = 2>
 struct ListLoader {
   int64_t raw[2];  // what begin() asked for
   float raw_t[2];
