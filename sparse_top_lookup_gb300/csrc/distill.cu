@@ -14,10 +14,10 @@
 // sum); short rows are held in the registers of a warp each.
 //
 // Softmax arithmetic is in powers of two: with c = log2(e) / T and the
-// largest logit m, the terms are 2^((z - m) c).  Where m c is in range they
-// are formed as 2^(z c - r), r = rn(m c), one instruction less; where it is
-// not (rows whose every logit is a mask's lowest value) the difference comes
-// first.
+// largest logit m, the terms are 2^((z - m) c).  Where |m c| < 2^24 the sums
+// form them as 2^(z c - r), r = rn(m c), one instruction less, and 2^(r - m c)
+// at the end, within 2^(1/2) of 1; further out (masked stretches, tiny T) what
+// r leaves of m c grows to powers that overflow, and the difference comes first.
 //
 // Measured, GB/s of logits read and dz written (a copy reaches 6802): training step fp32 4096 x
 // 65536 6460 (95 %), bf16 4096 x 131072 with lists of 64 6340 (93 %), loss alone, bf16 4096 x
@@ -578,7 +578,8 @@ __device__ __forceinline__ void add_vectors(Sum& sum, const uint4 (&d)[kNV], flo
   sum = Sum{m, (sa.x + sa.y) + (sb.x + sb.y)};
 }
 // The same for `count` vectors in shared memory, kThreads apart, as 2^(z c - r), r = rn(m c),
-// and one factor 2^(r - m c) for them all; one by one in the form above when m c is out of range.
+// and one factor 2^(r - m c) for them all; one by one in the form above from |m c| = 2^24 on, where
+// r is off by more than half.
 template <typename E, int kThreads>
 __device__ __forceinline__ void add_shared(Sum& sum, const uint4* src, int count, float c) {
   constexpr int kPer = El<E>::kPerVec;
@@ -587,7 +588,7 @@ __device__ __forceinline__ void add_shared(Sum& sum, const uint4* src, int count
   for (int j = 0; j < count; ++j) most.add(src[j * kThreads]);
   const float m = fmaxf(sum.m, most.value());
   const float r = m * c;
-  if (!(fabsf(r) < 1e37f)) {
+  if (!(fabsf(r) < 16777216.0f)) {
 #pragma unroll 1
     for (int j = 0; j < count; ++j) {
       const uint4 one[1] = {src[j * kThreads]};
