@@ -362,21 +362,26 @@ __device__ void put_loss(const DistillArgs& a, int64_t b, const Sum& sum, const 
   }
 }
 
+// The fast forms of a gradient take the row's reference in the exponent of 2^(z c + off), off of
+// magnitude below this (a limit of 2^24 would do for fp32, where only the rest of off's rounding
+// matters; the difference first costs one instruction more per logit).
+constexpr float kFastOff = 1024.0f;
+
 // g q(z) of a row, from its sum; every q is 0 when every logit is -inf.  With the factor
-// 2^(z c + off) ahead of `scale` the difference z - ref costs no instruction; rows whose
-// reference is so far out that ref c overflows (all logits at a mask's value) are `far` and take
-// the difference first.  For bf16 the factor |scale| goes into the exponent too (off_all; 2^-19
-// at most for it, where dz is rounded to 2^-8), and its sign into the packed result.  What the
-// rounding of off leaves is in scale_fast.
+// 2^(z c + off) ahead of `scale` the difference z - ref costs no instruction; what the rounding of
+// off leaves is in scale_fast.  For bf16 the factor |scale| goes into the exponent too (off_all,
+// rounded by 2^-14 / 2 at most below kFastOff, where dz is rounded to 2^-8), and its sign into the
+// packed result.  Rows further out (masked stretches, a common offset, tiny T) are `far` and take
+// the difference first.
 struct Grad {
   float c, ref, scale, scale_fast, off, off_all;
   bool far;
   Grad() = default;
   __device__ Grad(float c, float ref, float scale) : c(c), ref(ref), scale(scale) {
     off = -ref * c;
-    far = !(fabsf(off) < 1e37f);
     scale_fast = scale * ex2(fmaf(-ref, c, -off));
     off_all = off + log2f(fabsf(scale_fast));
+    far = !(fabsf(off) < kFastOff && fabsf(off_all) < kFastOff);
   }
   __device__ float operator()(float z) const { return ex2((z - ref) * c) * scale; }
   __device__ float fast(float z) const { return ex2(fmaf(z, c, off)) * scale_fast; }

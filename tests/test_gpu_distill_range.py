@@ -174,3 +174,41 @@ def test_losses_of_tiny_temperatures(B, V, dtype, T):
     for loss, lse in (forward(z, idx, t, T), train(z, idx, t, T, dl)[:2]):
         within(lse, e.lse, 2 * U * e.lse.abs() + 64 * U, "lse")
         within(loss, e.loss, 64 * U * (e.loss.abs() + T), "loss")
+
+
+def check_train(z, idx, t, dl, T):
+    e = Exact(z, idx, t, T, dl)
+    err = e.dz_err(e.rel_q, z.dtype)
+    within(train(z, idx, t, T, dl)[2], e.dz, err, "dz")
+    B, V = z.shape
+    d, loss, lse = z.clone(), torch.empty(B, device="cuda"), torch.empty(B, device="cuda")
+    pk.check(pk.pkm_distill_train(d, KIND[z.dtype], V, B, V, idx, t, idx.shape[1], T, dl, loss, lse, d, V),
+             "train in place")
+    within(d, e.dz, err, "dz in place")
+
+
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("where", WHERE)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", FORMS)
+def test_training_gradients_of_rows_with_finite_masks(B, V, dtype, where, value):
+    for T in (1.0, 1.7):
+        check_train(*masked(B, V, dtype, where, value), T)
+
+
+@pytest.mark.parametrize("offset", [300.0, 1e3, -1e3, 1e4, 1e5, 1e6, -1e6, 1e10, 1e30])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", FORMS)
+def test_training_gradients_of_rows_with_a_common_offset(B, V, dtype, offset):
+    z, idx, t, dl = rows(B, V, F32, 2)
+    check_train((z + offset).to(dtype), idx, t, dl, 0.7)
+
+
+@pytest.mark.parametrize("T", [1e-2, 1e-3, 1e-6, 1e-10, 1e-20])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", FORMS)
+def test_training_gradients_of_tiny_temperatures(B, V, dtype, T):
+    z, idx, t, dl = rows(B, V, dtype, 3)
+    t = t.round() + torch.arange(4, device="cuda") * 0.25
+    z[:, 7] = 30.0
+    check_train(z, idx, t, dl, T)
