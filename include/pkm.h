@@ -517,7 +517,7 @@ int pkm_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up,
  * a list that names such a column with p > 0 has an infinite loss.  k up to
  * PKM_DISTILL_MAX_K.  lse is fp32: where a row's logits are all so far from zero
  * (10^5 T and more, as when every one is a mask of a large negative value) that lse cannot hold
- * log V beside them, pkm_distill_backward's q is no better than that, while
+ * log V beside them, pkm_distill_backward's q is no better than that (within [0, 1]), while
  * pkm_distill_train's is exact (for V up to 262144 of bf16 or 131072 of fp32; longer rows go through the
  * other two).
  *

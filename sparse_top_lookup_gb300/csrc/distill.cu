@@ -390,25 +390,32 @@ __device__ __forceinline__ Grad grad_of(const Sum& sum, float g, float c) {
   const float ref = sum.m == -INFINITY ? 0.0f : sum.m;
   return Grad(c, ref, sum.s == 0.0f ? 0.0f : __fdividef(g, sum.s));
 }
-// From an lse in fp32: q = exp(z / T - lse).  In the far rows lse holds no more than the row's
-// maximum; q stays within [0, 1] there.
+// From an lse in fp32: q = exp(z / T - lse).  The forms are Grad's.  Far rows keep q within [0, 1],
+// which an lse so rounded says no more about (from 10^5 T on; at a mask's value of -10^9 it holds
+// the row's maximum alone): off is a quarter there, so that any lse has one, and off_all what its
+// rounding leaves.
 struct GradLse {
   float c, scale, off, off_all;
   bool far;
   __device__ GradLse(float lse, float g, float c) : c(c) {
     // (a row whose lse is NaN or +inf has no gradient)
     scale = lse < INFINITY ? g : NAN;
+    if (lse == -INFINITY) lse = 0.0f;  // every logit is -inf, or beyond fp32: q is 0
     off = -lse * kLog2e;
-    far = !(fabsf(off) < 1e37f);
-    if (far)
+    const float scale_fast = scale * ex2(fmaf(-lse, kLog2e, -off));
+    off_all = off + log2f(fabsf(scale_fast));
+    far = !(fabsf(off) < kFastOff && fabsf(off_all) < kFastOff);
+    if (far) {
       off = -lse * (0.25f * kLog2e);
-    else
-      scale *= ex2(fmaf(-lse, kLog2e, -off));
-    if (lse == -INFINITY) scale = g, off = 0.0f, far = false;
-    off_all = off + log2f(fabsf(scale));
+      off_all = fmaf(-lse, 0.25f * kLog2e, -off);
+    } else {
+      scale = scale_fast;
+    }
   }
   __device__ float operator()(float z) const {
-    return (far ? ex2(fminf(4.0f * fmaf(z, 0.25f * c, off), 0.0f)) : ex2(fmaf(z, c, off))) * scale;
+    if (!far) return fast(z);
+    const float e = 4.0f * (fmaf(z, 0.25f * c, off) + off_all);
+    return ex2(e > 0.0f ? 0.0f : e) * scale;
   }
   __device__ float fast(float z) const { return ex2(fmaf(z, c, off)) * scale; }
 };

@@ -212,3 +212,47 @@ def test_training_gradients_of_tiny_temperatures(B, V, dtype, T):
     t = t.round() + torch.arange(4, device="cuda") * 0.25
     z[:, 7] = 30.0
     check_train(z, idx, t, dl, T)
+
+
+def check_backward(z, idx, t, dl, T):
+    """From an lse rounded to fp32: to that rounding; where it says nothing, q within [0, 1]."""
+    e = Exact(z, idx, t, T, dl)
+    B, V = z.shape
+    lse, dz = e.lse.float(), torch.empty_like(z)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pk.check(pk.pkm_distill_backward(z, KIND[z.dtype], V, B, V, idx, t, idx.shape[1], T, lse, dl, dz, V, st),
+             "backward")
+    assert st.item() == pk.PKM_OK
+    far = 4 * U * e.lse.abs()[:, None]
+    err = e.dz_err(torch.expm1(e.rel_q.clamp(max=1.0) + far.clamp(max=1.0)), z.dtype)
+    most = e.scale * (1 + e.P) * (1 + 2.0 ** -7)
+    known = (far < 0.1).expand_as(dz)
+    within(dz[known], e.dz[known], err[known], "dz")
+    within(dz, torch.zeros_like(e.dz), most, "dz's range")
+
+
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("where", WHERE)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", FORMS)
+def test_gradients_from_lse_of_rows_with_finite_masks(B, V, dtype, where, value):
+    for T in (1.0, 1.7):
+        check_backward(*masked(B, V, dtype, where, value), T)
+
+
+@pytest.mark.parametrize("offset", [300.0, 1e3, -1e3, 1e4, 1e5, 1e6, -1e6, 1e7, 1e8, -1e8, 1e10, 1e30])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", FORMS)
+def test_gradients_from_lse_of_rows_with_a_common_offset(B, V, dtype, offset):
+    z, idx, t, dl = rows(B, V, F32, 2)
+    check_backward((z + offset).to(dtype), idx, t, dl, 0.7)
+
+
+@pytest.mark.parametrize("T", [1e-2, 1e-3, 1e-6, 1e-10, 1e-20])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,V", FORMS)
+def test_gradients_from_lse_of_tiny_temperatures(B, V, dtype, T):
+    z, idx, t, dl = rows(B, V, dtype, 3)
+    t = t.round() + torch.arange(4, device="cuda") * 0.25
+    z[:, 7] = 30.0
+    check_backward(z, idx, t, dl, T)
