@@ -804,6 +804,12 @@ distill_backward_kernel(const DistillArgs a) {
 //   i + 2 L after its grad(i + L), for which this CTA has sent i + L: both come after all that
 //   the list warp of row i does for it but its listed columns, which need its own copies only.
 // In kFwd, without second passes, data warps wait for sums(i - L) before they write their sum i.
+//
+// Giving up.  A warp whose wait runs out, or that sees that another's did, sends and writes nothing
+// more.  The list warps end at a barrier of the cluster on every path, so a CTA's memory stays while
+// any other may send to it (threads that have left count as arrived: the other warps just leave).
+// What a list warp has sent has landed by then: it waits for the sums of its last row from all
+// CTAs, which wait for its own in turn, or until that wait has run out too.
 constexpr int kListWarps = 3;
 constexpr int kCopies = 2 * kListWarps;
 constexpr int kMaxSlots = 16;
@@ -927,10 +933,10 @@ distill_stream_kernel(const DistillArgs a) {
     }
     return;
   }
-  // the row's sum, once every slice's has come
+  // Waits of a whole warp; false: gave up.  wait_sums: every slice's sum of row i has come.
+  auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
   auto wait_sums = [&](int i) {
-    wait_phase_cluster(bar_sums(i), (uint32_t)(i / kCopies) & 1u, ctl);
-    __syncwarp();
+    return all(wait_phase_cluster(bar_sums(i), (uint32_t)(i / kCopies) & 1u, ctl));
   };
   auto sum_of = [&](int i) {
     return lanes_join<kMaxSlices>(lane % kMaxSlices < slices
@@ -961,12 +967,13 @@ distill_stream_kernel(const DistillArgs a) {
     if (wanted(h)) loader.begin(a, row_at(h), lane);
     ask(h);
     load(h);
+    int sent = -1;  // the last row whose sum was sent
     // (kTrain: as many rows more, for the listed columns of the last)
     for (int i = h; i < count + (kMode == kTrain ? kListWarps : 0); i += kListWarps) {
       const Sum ls = ls_next;
-      wait_phase(bar_local(i), (uint32_t)(i / kCopies) & 1u, ctl);
-      __syncwarp();
+      if (!all(wait_phase(bar_local(i), (uint32_t)(i / kCopies) & 1u, ctl))) break;
       if (i < count) {
+        sent = i;
         const Sum sum = lanes_join<kData>(s_warp[i % kCopies][lane & (kData - 1)], c);
         // to every CTA of the cluster (this one too), completing on the receiver's barrier
         if (lane == 0) mbar_expect_tx(bar_sums(i), 8u * slices);
@@ -980,7 +987,7 @@ distill_stream_kernel(const DistillArgs a) {
       }
       if (kMode == kTrain && i < count) {
         const float g = s_geo[i % kCopies].g;
-        wait_sums(i);
+        if (!wait_sums(i)) break;
         const Grad q = grad_of(sum_of(i), g, c);
         if (lane == 0) {
           s_grad[i % kCopies] = RowGrad{q, g, g == 0.0f || ls.m == -INFINITY};
@@ -998,12 +1005,14 @@ distill_stream_kernel(const DistillArgs a) {
       __syncwarp();
       load(i + kListWarps);
       if (i < count && my_loss(i)) {
-        wait_sums(i);
+        if (!wait_sums(i)) break;
         put_loss(a, row_at(i), sum_of(i), list_at(i % kCopies), ls, lane);
       }
     }
-    // the other CTAs' last sums are here before this CTA's memory goes
-    for (int i = max(0, count - kListWarps); i < count; ++i) wait_sums(i);
+    // the other CTAs' last sums are here (earlier ones came before that row's were sent)
+    if (sent >= 0) wait_phase_drain(bar_sums(sent), (uint32_t)(sent / kCopies) & 1u);
+    __syncwarp();
+    if (slices > 1) cluster_sync();
     return;
   }
   // ------------------------------------------------------------------ data
@@ -1014,7 +1023,7 @@ distill_stream_kernel(const DistillArgs a) {
     x_last = x;
     if (i < count) {
       Sum sum{-INFINITY, 0.0f};
-      if (!__all_sync(0xffffffffu, wait_phase(bar_full(s1), ph, ctl))) return;  // (gave up)
+      if (!all(wait_phase(bar_full(s1), ph, ctl))) return;  // (gave up)
       const Geo<E>& geo = s_geo[i % kCopies];
       const int total = geo.n;
       x = -INFINITY;
@@ -1029,11 +1038,11 @@ distill_stream_kernel(const DistillArgs a) {
         }
         if (++s1 == slots) s1 = 0, ph ^= 1u;
         if ((v += chunk) >= total) break;
-        wait_phase(bar_full(s1), ph, ctl);
+        if (!all(wait_phase(bar_full(s1), ph, ctl))) return;
       }
       if (geo.ends) add_one(sum, x, c);
       sum = lanes_join<32>(sum, c);
-      if (kMode == kFwd && i >= kListWarps) wait_sums(i - kListWarps);
+      if (kMode == kFwd && i >= kListWarps && !wait_sums(i - kListWarps)) return;
       if (lane == 0) {
         s_warp[i % kCopies][warp] = sum;
         mbar_arrive(bar_local(i));
@@ -1043,8 +1052,7 @@ distill_stream_kernel(const DistillArgs a) {
     }
     if (kMode == kTrain && i > 0) {
       const Geo<E>& geo = s_geo[(i - 1) % kCopies];
-      wait_phase(bar_grad(i - 1), (uint32_t)((i - 1) / kCopies) & 1u, ctl);
-      __syncwarp();
+      if (!all(wait_phase(bar_grad(i - 1), (uint32_t)((i - 1) / kCopies) & 1u, ctl))) return;
       const bool zero = s_grad[(i - 1) % kCopies].zero;
       const Grad q = s_grad[(i - 1) % kCopies].q;
       E* body = geo.body;
