@@ -342,13 +342,15 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
         if (k0 >= q.K) k0 = 0, ++seg;
       }
     }
-    // the leader's last releases of this CTA's stages land before it exits
-    if (ok)
-      for (uint32_t j = 0; j < used; ++j) {
-        if (s == 0) s = FSTAGES, ph ^= 1u;
-        --s;
-        wait_phase_drain(bar_empty(s), ph ^ 1u);
-      }
+    // the leader's last releases of this CTA's stages land before it exits; if a wait gave up, the
+    // copies on their way (the leader sees both CTAs', as far as it has got)
+    if (!ok && rank != 0) let_copies_land();
+    for (uint32_t j = 0; (ok || rank == 0) && j < used; ++j) {
+      if (s == 0) s = FSTAGES, ph ^= 1u;
+      --s;
+      wait_phase_drain(ok ? bar_empty(s) : bar_full(s), ph ^ 1u);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader)
     if (rank == 0) {
@@ -402,8 +404,10 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
     const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t bufs = stages_u32 + FSTAGES * FSTAGE_BYTES + ew * Shape::kOut;
     uint32_t nb = 0;  // next buffer of four; kDGate: bit k, the parity of set k's next loads
+    uint32_t asked = 0;  // kDGate, lane 0: bit k, set k's loads are on their way
+    bool ok = true;
     Seg sg;
-    for (int i = 0; seg_at(p.plan, slot, i, sg); ++i) {
+    for (int i = 0; ok && seg_at(p.plan, slot, i, sg); ++i) {
       int tm, tn;
       const Prod& q = tile_at<kTileN>(p, sg.tile, tm, tn);
       const int M = q.M, N = q.N;
@@ -427,6 +431,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       auto ask = [&](int c) {
         const uint32_t k = (c >> 5) & 1, set = bufs + k * 3 * 2048;
         blocks_read<0>();  // the set's stores are done with it
+        asked |= 1u << k;
         mbar_expect_tx(bar_set + 8u * k, 2 * 2048);
         tma_load_2d(set, &p.in[0], col0 + c, row0, bar_set + 8u * k);
         tma_load_2d(set + 2048, &p.in[1], col0 + c, row0, bar_set + 8u * k);
@@ -436,7 +441,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
         if (cols > 32) ask(32);
       }
       __syncwarp();
-      if (!__all_sync(0xffffffffu, wait_phase_cluster(bar_tfull(buf), use & 1u, ctl))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_phase_cluster(bar_tfull(buf), use & 1u, ctl)))) break;
       tc_fence_after();
       if (row0 < M && cols > 0) {
         if (sg.part >= 0) {
@@ -473,9 +478,10 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
                   break;
                 }
               } while (f != p.epoch && !*ctl.abort);
+              if (f != p.epoch) ok = false;
               *flag = 0;  // the next launch with this workspace starts afresh
             }
-            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
           }
           // accumulator columns tc .. tc + 31, with the other stretches' parts
           auto sums = [&](int tc, float (&v)[32]) {
@@ -495,7 +501,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
             nb = (nb + 1) & 3;
             return b;
           };
-          for (int c = 0; c < cols; c += 32) {
+          for (int c = 0; ok && c < cols; c += 32) {
             const int tc = half * kHalfN + c, gc = col0 + c;
             float v[32];
             if constexpr (kEpi == kGate) {
@@ -555,8 +561,10 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               const uint32_t k = (c >> 5) & 1, b0 = bufs + k * 3 * 2048, b1 = b0 + 2048,
                              b2 = b1 + 2048;
               sums(tc, v);
-              if (!__all_sync(0xffffffffu, wait_phase(bar_set + 8u * k, (nb >> k) & 1u, ctl))) break;
+              if (!(ok = __all_sync(0xffffffffu, wait_phase(bar_set + 8u * k, (nb >> k) & 1u, ctl))))
+                break;
               nb ^= 1u << k;
+              asked &= ~(1u << k);
               float g[32], u[32];
               get_row(b0, lane, g);
               get_row(b1, lane, u);
@@ -591,7 +599,11 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(bar_tempty(buf), 0));
     }
-    if (lane == 0) blocks_written();
+    if (lane == 0) {
+      for (uint32_t k = 0; kEpi == kDGate && k < 2; ++k)  // (gave up before they were needed)
+        if (asked >> k & 1u) wait_phase_drain(bar_done + 8u * (1 + 2 * ew + k), (nb >> k) & 1u);
+      blocks_written();
+    }
   }
 
   tc_fence_before();

@@ -374,6 +374,13 @@ __device__ __forceinline__ void wait_phase_drain(uint32_t bar, uint32_t parity) 
     if (globaltimer() - t0 > WAIT_LIMIT_NS) return;
 }
 
+// After a wait has given up: time for copies to land that this CTA cannot wait for, those that
+// signal its pair's leader (1 ms; a copy takes a few us).
+__device__ __forceinline__ void let_copies_land() {
+  const unsigned long long t0 = globaltimer();
+  while (globaltimer() - t0 < 1000000ull) {
+  }
+}
 
 // ------------------------------------------------------------------ host
 

@@ -61,3 +61,15 @@ def test_every_path_of_those_that_stay_ends_at_the_clusters_last_barrier(body):
         depth += {"}": 1, "{": -1}.get(body[start], 0)
     between = body[max(start, body.index("cluster_sync()")):last]
     assert not re.search(r"\breturn\b", between)
+
+
+# what each kernel's copies signal: on its way out a warp that gave up waits (with a limit) for these too
+COPIES = [("ffn.cu", "ffn_gemm_kernel", ["bar_full", "bar_set|bar_done \\+ 8u"]),
+          ("distill.cu", "distill_stream_kernel", ["bar_full", "bar_sums"])]
+
+
+@pytest.mark.parametrize("name,kernel,barriers", COPIES, ids=[k for _, k, _ in COPIES])
+def test_copies_on_their_way_are_waited_for(name, kernel, barriers):
+    body = {(f, k): b for f, k, b in kernels()}[name, kernel]
+    for b in barriers:
+        assert re.search(r"wait_phase_drain\([^;]*(%s)" % b, body), b
