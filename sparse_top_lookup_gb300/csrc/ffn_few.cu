@@ -212,8 +212,10 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.g_in + o));
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.u_in + o));
     }
-  // every copy has landed and every MMA has read it: the ring takes the sums, [token][row]
-  wait_phase(bar_done, 0, ctl);
+  // every copy has landed and every MMA has read it: the ring takes the sums, [token][row] (those of a
+  // call that gave up mean nothing, but its MMAs still end before their memory goes)
+  if (!wait_phase(bar_done, 0, ctl)) wait_phase_drain(bar_done, 0);
+  __syncwarp();
   tc_fence_after();
   __syncthreads();
   if (warp >= 2) {
