@@ -479,7 +479,7 @@ enum {
   PKM_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
   PKM_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
   PKM_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
-  PKM_ACT_RELU = 3       /* max(g, 0), slope 0 at 0 */
+  PKM_ACT_RELU = 3       /* max(g, 0), slope 0 at 0; a NaN stays one, as in the others */
 };
 size_t pkm_gated_ffn_workspace_bytes(int B, int dim, int F);
 int pkm_gated_ffn(const void *x, const void *w_gate, const void *w_up, const void *w_down, int B,

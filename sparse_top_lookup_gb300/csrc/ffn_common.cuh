@@ -43,7 +43,8 @@ __device__ __forceinline__ float2 act_both(float g) {
     const float s = sigmoid2(kTanh * kLog2e * g * fmaf(0.044715f, g2, 1.0f)), a = g * s;
     return make_float2(a, fmaf(a * (1.0f - s), kTanh * fmaf(0.134145f, g2, 1.0f), s));
   } else {
-    return make_float2(fmaxf(g, 0.0f), g > 0.0f ? 1.0f : 0.0f);
+    // (a NaN stays one, as in the other activations)
+    return g <= 0.0f ? make_float2(0.0f, 0.0f) : make_float2(g, g > 0.0f ? 1.0f : g);
   }
 }
 template <int kAct>
