@@ -36,8 +36,20 @@ __device__ __forceinline__ float2 act_both(float g) {
     const float s = sigmoid2(g * kLog2e), a = g * s;
     return make_float2(a, fmaf(a, 1.0f - s, s));
   } else if constexpr (kAct == PKM_ACT_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(g * 0.70710678f));
-    return make_float2(g * cdf, fmaf(g * 0.39894228f, ex2(g * g * (-0.5f * kLog2e)), cdf));
+    // The normal distribution's cdf, good relative to itself in the negative tail, where
+    // (1 + erf) / 2 cancels (at g = -5 it is 3e-7): exp(-g^2 / 2), which the slope needs anyway,
+    // times a polynomial in 1 / (1 + 0.3625 |g|), fitted over |g| < 13.5 for the least largest
+    // relative error (2^-20; 2^-17 with the exponent's rounding).  Forward 16384 x 1024 x 4096: 229 us
+    // with erff, 270 with erfcf, 225 so.
+    const float e = ex2(g * g * (-0.5f * kLog2e)), t = rcp(fmaf(0.3625f, fabsf(g), 1.0f));
+    float r = fmaf(t, 0.0480628908f, -0.179742411f);
+    r = fmaf(t, r, 0.175103992f);
+    r = fmaf(t, r, 0.0296824165f);
+    r = fmaf(t, r, 0.139256716f);
+    r = fmaf(t, r, 0.142936394f);
+    r = fmaf(t, r, 0.144700378f);
+    const float tail = e * (t * r), cdf = g < 0.0f ? tail : 1.0f - tail;
+    return make_float2(g * cdf, fmaf(g * 0.39894228f, e, cdf));
   } else if constexpr (kAct == PKM_ACT_GELU_TANH) {
     const float g2 = g * g;
     const float s = sigmoid2(kTanh * kLog2e * g * fmaf(0.044715f, g2, 1.0f)), a = g * s;
