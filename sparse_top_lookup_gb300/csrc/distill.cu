@@ -1125,21 +1125,27 @@ struct Launch {
   Launch(const Launch&) = delete;
 };
 
+// Vectors of a row at most (V up to the largest int).
+template <typename E>
+int64_t vectors_of(int V) {
+  return ((int64_t)V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+}
+
 template <typename E, int kNV, int kMode>
 cudaError_t launch_warps(const DistillArgs& a, cudaStream_t stream) {
   static int most = 0;
   auto kernel = distill_warp_kernel<E, kNV, kMode>;
   cudaError_t e = resident_ctas(&most, kernel, DTHREADS, (size_t)DWARPS * kWarpMaxK * kListBytes);
   if (e != cudaSuccess) return e;
-  const int ctas = (a.B + DWARPS - 1) / DWARPS;
-  const Launch l(ctas < most ? ctas : most, DTHREADS, (size_t)DWARPS * kListBytes * a.kpad, 1,
+  const int64_t ctas = ((int64_t)a.B + DWARPS - 1) / DWARPS;
+  const Launch l((unsigned)(ctas < most ? ctas : most), DTHREADS, (size_t)DWARPS * kListBytes * a.kpad, 1,
                  stream);
   return cudaLaunchKernelEx(&l.cfg, kernel, a);
 }
 
 template <typename E>
 cudaError_t launch_backward(DistillArgs& a, cudaStream_t stream) {
-  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+  const int64_t nvec = vectors_of<E>(a.V);
   while (nvec > (int64_t)kBwdVecs * DTHREADS << a.lsh) ++a.lsh;
   static int most = 0;
   auto kernel = distill_backward_kernel<E>;
@@ -1190,7 +1196,7 @@ cudaError_t launch_stream(const DistillArgs& a, cudaStream_t stream) {
 
 template <typename E, int kMode>
 cudaError_t dispatch_stream(DistillArgs& a, cudaStream_t stream) {
-  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+  const int64_t nvec = vectors_of<E>(a.V);
   // slices of at most 32 KB; more and smaller ones while CTAs are few
   while (a.lsh < kMaxLsh && nvec > (int64_t)kChunkVecs << a.lsh) ++a.lsh;
   while (a.lsh < kMaxLsh && ((int64_t)a.B << a.lsh) * 2 <= tc::sm_count() &&
@@ -1214,7 +1220,7 @@ cudaError_t dispatch(DistillArgs& a, cudaStream_t stream) {
   a.kpad = (a.k + 3) / 4 * 4;
   a.lsh = 0;
   // rows of up to 4 KB, when there are enough of them to fill the GPU: a warp each
-  const int64_t nvec = (a.V + El<E>::kPerVec - 1) / El<E>::kPerVec;
+  const int64_t nvec = vectors_of<E>(a.V);
   if (nvec <= 32 * 8 && a.k <= kWarpMaxK && a.B >= 4 * tc::sm_count())
     return nvec <= 32 * 2 ? launch_warps<E, 2, kMode>(a, stream)
                           : launch_warps<E, 8, kMode>(a, stream);
