@@ -112,9 +112,7 @@ struct GemmArgs {
   CUtensorMap in[2];    // kDGate: g, u
   int prods, act, keep;  // keep: kGate writes g and u
   Plan plan;
-  const __nv_bfloat16 *g_in, *u_in;  // kDGate
-  float4* parts;                // [stretch][CTA of the pair][column / 4][row], part_rows rows
-  int part_rows;
+  float4* parts;                // [stretch][CTA of the pair][column / 4][row], FM rows
   unsigned long long* flags;    // [stretch][CTA of the pair][epilogue warp]
   unsigned long long epoch;     // a flag's value when its part is there
   int* status;  // may be NULL
@@ -422,7 +420,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
       // this thread's part of a stretch's sums: [column / 4][row]
       const int prow = quad * 32 + lane;
       auto part_at = [&](int r) {
-        return p.parts + ((size_t)(2 * r + rank) * (kN / 4)) * p.part_rows + prow;
+        return p.parts + ((size_t)(2 * r + rank) * (kN / 4)) * FM + prow;
       };
       auto flag_at = [&](int r) { return p.flags + (size_t)(2 * r + rank) * FEPI_WARPS + ew; };
 
@@ -455,7 +453,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               if (in)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  __stcg(dst + (size_t)(tc / 4 + j) * p.part_rows,
+                  __stcg(dst + (tc / 4 + j) * FM,
                          make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
             }
           }
@@ -491,7 +489,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               if (in)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                  const float4 t = __ldcg(src + (size_t)(tc / 4 + j) * p.part_rows);
+                  const float4 t = __ldcg(src + (tc / 4 + j) * FM);
                   v[4 * j] += t.x, v[4 * j + 1] += t.y, v[4 * j + 2] += t.z, v[4 * j + 3] += t.w;
                 }
             }
@@ -651,20 +649,14 @@ bool result(CUtensorMap* m, void* ptr, int rows, int cols, bool f32 = false) {
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Parts of cut tiles, of products with at most M rows: [cluster][2][columns / 4][rows] float4, and
-// their flags.
+// Parts of cut tiles: [cluster][2][columns / 4][FM rows] float4, and their flags.
 constexpr int kMaxClusters = 80, kMaxN = 256;
-int part_rows(int M) { return M >= FM ? FM : (M + 31) / 32 * 32; }
-size_t parts_bytes(int M) {
-  return align256((size_t)kMaxClusters * 2 * kMaxN * part_rows(M) * 4) +
-         align256((size_t)kMaxClusters * 2 * FEPI_WARPS * 8);
-}
-void set_parts(GemmArgs& p, void* ws, int M) {
-  p.part_rows = part_rows(M);
+constexpr size_t kPartsBytes = (size_t)kMaxClusters * 2 * kMaxN * FM * 4;
+constexpr size_t kFlagsBytes = (size_t)kMaxClusters * 2 * FEPI_WARPS * 8;
+static_assert(kPartsBytes % 256 == 0 && kFlagsBytes % 256 == 0, "parts of the workspace are aligned");
+void set_parts(GemmArgs& p, void* ws) {
   p.parts = static_cast<float4*>(ws);
-  p.flags = reinterpret_cast<unsigned long long*>(
-      static_cast<unsigned char*>(ws) +
-      align256((size_t)kMaxClusters * 2 * kMaxN * p.part_rows * 4));
+  p.flags = reinterpret_cast<unsigned long long*>(static_cast<unsigned char*>(ws) + kPartsBytes);
 }
 
 // The value of this launch's flags.  The workspace is whatever its memory held before: a flag
@@ -805,10 +797,10 @@ cudaError_t launch_gemm(GemmArgs& p, const BOperand (&b)[kMaxProds][2], cudaStre
 }  // namespace
 
 size_t gated_ffn_workspace_bytes(int B, int F) {
-  return align256((size_t)B * F * 2) + (B > kFewTokens ? parts_bytes(B) : 0);
+  return align256((size_t)B * F * 2) + (B > kFewTokens ? kPartsBytes + kFlagsBytes : 0);
 }
 size_t gated_ffn_backward_workspace_bytes(int B, int F) {
-  return 3 * align256((size_t)B * F * 2) + parts_bytes(FM);
+  return 3 * align256((size_t)B * F * 2) + kPartsBytes + kFlagsBytes;
 }
 
 cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up,
@@ -822,7 +814,7 @@ cudaError_t launch_gated_ffn(const void* x, const void* w_gate, const void* w_up
   p.act = act;
   p.status = status;
   p.keep = gate != nullptr;
-  set_parts(p, static_cast<unsigned char*>(workspace) + align256((size_t)B * F * 2), B);
+  set_parts(p, static_cast<unsigned char*>(workspace) + align256((size_t)B * F * 2));
   Prod& q = p.prod[0];
   q.segs = 1;
   q.M = B, q.N = F, q.K = dim;
@@ -850,9 +842,7 @@ cudaError_t launch_gated_ffn_backward(const void* x, const void* w_gate, const v
   p.prods = 1;
   p.act = act;
   p.status = status;
-  p.g_in = static_cast<const __nv_bfloat16*>(gate);
-  p.u_in = static_cast<const __nv_bfloat16*>(up);
-  set_parts(p, ws + 3 * part, FM);
+  set_parts(p, ws + 3 * part);
   const bool few = B <= kFewTokens;
   if (few) {
     cudaError_t e = launch_ffn_few_backward(w_gate, w_up, w_down, gate, up, dy, B, dim, F, act, dg,
