@@ -26,6 +26,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "num_common.cuh"
 #include "pkm_internal.cuh"
 #include "tc_common.cuh"
 
@@ -36,7 +37,6 @@ using tc::cluster_ctarank;
 using tc::mapa_shared;
 using tc::smem_u32;
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int DTHREADS = 256;
 constexpr int DWARPS = DTHREADS / 32;
 constexpr int kMaxLsh = 3, kMaxSlices = 1 << kMaxLsh;  // CTAs of a cluster (the portable limit)
@@ -95,12 +95,6 @@ struct El<__nv_bfloat16> {
   };
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Two fp32 operations in one instruction, each rounded as by itself (the loss of 4096 x 131072 bf16:
 // 167 us one by one, 159 so).
 struct Two {
@@ -119,11 +113,6 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
 __device__ __forceinline__ Two add2(Two a, Two b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
   return a;
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 w = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&w);
 }
 
 // A positive s as f 2^e, f in [0.75, 1.5): its log is e log 2 + logf(f), to about 1e-8 when the

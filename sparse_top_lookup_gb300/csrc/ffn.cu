@@ -616,22 +616,10 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
   }
 }
 
-// A [rows, cols] bf16 matrix in boxes of box_cols x box_rows, 128-byte swizzle.
-bool encode2(CUtensorMap* m, const void* ptr, int rows, int cols, int box_cols, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  const cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
-             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 // An operand whose rows are M (N) and whose columns are K, or the transpose; `rows` of it (64 for
 // the transpose) are one CTA's in a slab.
 bool operand(CUtensorMap* m, const void* ptr, int rows, int cols, bool mn, int box = FM) {
-  return encode2(m, ptr, rows, cols, 64, mn ? FK : box);
+  return encode_matrix(m, ptr, rows, cols, 64, mn ? FK : box);
 }
 // A result [rows, cols] in blocks of 32 x 32, bf16 or fp32.
 bool result(CUtensorMap* m, void* ptr, int rows, int cols, bool f32 = false) {

@@ -1,18 +1,15 @@
-// Activations of the gated feed-forward block and bf16 packing, shared by its kernels.
+// Activations of the gated feed-forward block, its matrices as TMA takes them: shared by its kernels.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <stdint.h>
 
 #include "../../include/pkm.h"
+#include "num_common.cuh"
+#include "tc_common.cuh"
 
 namespace pkm {
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -21,7 +18,6 @@ __device__ __forceinline__ float rcp(float x) {
 // 1 / (1 + exp(-x)), with x log2(e) given
 __device__ __forceinline__ float sigmoid2(float x2) { return rcp(1.0f + ex2(-x2)); }
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanh = 1.5957691216057308f;  // 2 sqrt(2 / pi): (1 + tanh v) / 2 = sigmoid(2 v)
 
 // What calls without a status word report into (looked up by the kernels: the address costs the
@@ -80,11 +76,21 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
     f(ActTag<PKM_ACT_RELU>());
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// A [rows, cols] bf16 matrix in boxes of box_cols x box_rows, 128-byte swizzle.
+inline bool encode_matrix(CUtensorMap* m, const void* ptr, int rows, int cols, int box_cols,
+                          int box_rows) {
+  tc::EncodeTiledFn enc = tc::encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace pkm

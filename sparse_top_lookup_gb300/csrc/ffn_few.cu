@@ -284,18 +284,6 @@ ffn_few_kernel(const __grid_constant__ FewArgs p) {
   }
 }
 
-bool encode_rows(CUtensorMap* m, const void* ptr, int rows, int cols, int box_cols, int box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  const cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
-             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // A [rows, cols] matrix, cols a multiple of 64, as [cols / 64][rows][64].
 bool encode_slabs(CUtensorMap* m, const void* ptr, int rows, int cols, int box_rows, int slabs) {
   EncodeTiledFn enc = encode_fn();
@@ -343,10 +331,10 @@ cudaError_t launch_few(FewArgs& p, const void* w0, const void* w1, const void* t
   p.t3 = p.K % WK == 0 && p.slabs > 1;
   const void *w[2] = {w0, w1}, *t[2] = {t0, t1};
   for (int i = 0; i < 2; ++i) {
-    if (w[i] && !(p.w_mn ? encode_rows(&p.w[i], w[i], p.K, p.M, 64, WK)
-                         : encode_rows(&p.w[i], w[i], p.M, p.K, WK, p.R)))
+    if (w[i] && !(p.w_mn ? encode_matrix(&p.w[i], w[i], p.K, p.M, 64, WK)
+                         : encode_matrix(&p.w[i], w[i], p.M, p.K, WK, p.R)))
       return cudaErrorInvalidValue;
-    if (t[i] && !encode_rows(&p.t[i], t[i], p.T, p.K, WK, p.npad)) return cudaErrorInvalidValue;
+    if (t[i] && !encode_matrix(&p.t[i], t[i], p.T, p.K, WK, p.npad)) return cudaErrorInvalidValue;
     if (t[i] && p.t3 && !encode_slabs(&p.t3_map[i], t[i], p.T, p.K, p.npad, p.slabs))
       return cudaErrorInvalidValue;
   }
