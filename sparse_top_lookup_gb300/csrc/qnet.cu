@@ -488,12 +488,12 @@ qnet2_kernel(const __grid_constant__ CUtensorMap tmap_x,
                           fb);
         }
       }
-      // the leader's last releases of this CTA's stages land before it exits
-      if (ok) {
-        const uint32_t first = it > (uint32_t)Q2STAGES ? it - Q2STAGES : 0u;
-        for (uint32_t j = first; j < it; ++j)
-          wait_phase_drain(bar_empty(j % Q2STAGES), (j / Q2STAGES) & 1u);
-      }
+      // the leader's last releases of this CTA's stages land before it exits; if a wait gave up, the
+      // copies on their way (the leader sees both CTAs', as far as it has got)
+      if (!ok && rank != 0) let_copies_land();
+      const uint32_t first = it > (uint32_t)Q2STAGES ? it - Q2STAGES : 0u;
+      for (uint32_t j = first; (ok || rank == 0) && j < it; ++j)
+        wait_phase_drain(ok ? bar_empty(j % Q2STAGES) : bar_full(j % Q2STAGES), (j / Q2STAGES) & 1u);
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (leader)

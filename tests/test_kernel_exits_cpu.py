@@ -66,7 +66,9 @@ def test_every_path_of_those_that_stay_ends_at_the_clusters_last_barrier(body):
 # what each kernel's copies signal: on its way out a warp that gave up waits (with a limit) for these too
 COPIES = [("ffn_few.cu", "ffn_few_kernel", ["bar_full", "bar_done"]),  # (bar_done: its MMAs)
           ("ffn.cu", "ffn_gemm_kernel", ["bar_full", "bar_set|bar_done \\+ 8u"]),
-          ("distill.cu", "distill_stream_kernel", ["bar_full", "bar_sums"])]
+          ("distill.cu", "distill_stream_kernel", ["bar_full", "bar_sums"]),
+          ("lookup_2sm.cu", "select_2sm_kernel", ["bar_full"]),
+          ("qnet.cu", "qnet2_kernel", ["bar_full"])]
 
 
 @pytest.mark.parametrize("name,kernel,barriers", COPIES, ids=[k for _, k, _ in COPIES])
