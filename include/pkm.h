@@ -470,7 +470,8 @@ int pkm_query_net_batch(const void *x, const void *weight, int B, int dim, int F
  * (pkm_gated_ffn_backward_workspace_bytes).
  *
  * B == 0 is a no-op, except that bf16 weight gradients are set to zero.
- * status: as pkm_query_net's.  Errors: PKM_ERR_INVALID (NULL pointer, B < 0,
+ * status: as pkm_query_net's.  A captured call that gave up (PKM_ERR_TIMEOUT) may leave marks in its
+ * workspace: zero that before the graph is replayed.  Errors: PKM_ERR_INVALID (NULL pointer, B < 0,
  * dim < 1, F < 1, one of two that go together), PKM_ERR_UNSUPPORTED (dim or F
  * no multiple of 8, act, grad_dtype), PKM_ERR_RANGE (a product's tiles above
  * 2^31 - 1), PKM_ERR_ALIGN (a pointer not 16-byte aligned; status: 4), PKM_ERR_CUDA.

@@ -19,9 +19,9 @@
 // at the end, within 2^(1/2) of 1; further out (masked stretches, tiny T) what
 // r leaves of m c grows to powers that overflow, and the difference comes first.
 //
-// Measured, GB/s of logits read and dz written (a copy reaches 6802): training step fp32 4096 x
-// 65536 6460 (95 %), bf16 4096 x 131072 with lists of 64 6340 (93 %), loss alone, bf16 4096 x
-// 131072 6760 (99 %), backward pass bf16 4096 x 131072 6400 (94 %).
+// Measured, GB/s of logits read and dz written (a copy reaches 6802), ten calls in a graph: training
+// step fp32 4096 x 65536 6650 (98 %), bf16 4096 x 131072 with lists of 64 6390 (94 %), loss alone,
+// bf16 4096 x 131072 6840 (101 %), backward pass bf16 4096 x 131072 6490 (95 %).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -96,7 +96,7 @@ struct El<__nv_bfloat16> {
 };
 
 // Two fp32 operations in one instruction, each rounded as by itself (the loss of 4096 x 131072 bf16:
-// 167 us one by one, 159 so).
+// 167 us one by one, 159 so, when that was chosen).
 struct Two {
   unsigned long long v;
   __device__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
