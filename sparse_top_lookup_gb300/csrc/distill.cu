@@ -20,7 +20,7 @@
 // r leaves of m c grows to powers that overflow, and the difference comes first.
 //
 // Measured, GB/s of logits read and dz written (a copy reaches 6802), ten calls in a graph: training
-// step fp32 4096 x 65536 6650 (98 %), bf16 4096 x 131072 with lists of 64 6390 (94 %), loss alone,
+// step fp32 4096 x 65536 6650 (98 %), bf16 4096 x 131072 with lists of 64 6440 (95 %), loss alone,
 // bf16 4096 x 131072 6840 (101 %), backward pass bf16 4096 x 131072 6490 (95 %).
 #include <cuda_bf16.h>
 #include <math.h>
@@ -795,10 +795,11 @@ distill_backward_kernel(const DistillArgs a) {
 // In kFwd, without second passes, data warps wait for sums(i - L) before they write their sum i.
 //
 // Giving up.  A warp whose wait runs out, or that sees that another's did, sends and writes nothing
-// more.  The list warps end at a barrier of the cluster on every path, so a CTA's memory stays while
-// any other may send to it (threads that have left count as arrived: the other warps just leave).
-// What a list warp has sent has landed by then: it waits for the sums of its last row from all
-// CTAs, which wait for its own in turn, or until that wait has run out too.
+// more.  A list warp leaves when its last row's sums have come from every CTA, which is the last that
+// any sends to it; one that gave up ends at a barrier of the cluster instead, so that its CTA's memory
+// stays while another may send to it (threads that have left count as arrived).  What it has sent
+// itself has landed by then: it waits for that row's sums, whose senders wait for its own in turn, or
+// until that wait has run out too.  With the barrier on every path 4096 x 131072 bf16 took 336 us, so 333.
 constexpr int kListWarps = 3;
 constexpr int kCopies = 2 * kListWarps;
 constexpr int kMaxSlots = 16;
@@ -998,10 +999,14 @@ distill_stream_kernel(const DistillArgs a) {
         put_loss(a, row_at(i), sum_of(i), list_at(i % kCopies), ls, lane);
       }
     }
-    // the other CTAs' last sums are here (earlier ones came before that row's were sent)
-    if (sent >= 0) wait_phase_drain(bar_sums(sent), (uint32_t)(sent / kCopies) & 1u);
-    __syncwarp();
-    if (slices > 1) cluster_sync();
+    // Once its last row's sums have come from every CTA, none sends to this warp's barriers again
+    // (earlier rows' came before that row's were sent).
+    const bool done = sent < 0 ? h >= count : sent + kListWarps >= count && wait_sums(sent);
+    if (!done) {
+      if (sent >= 0) wait_phase_drain(bar_sums(sent), (uint32_t)(sent / kCopies) & 1u);
+      __syncwarp();
+      if (slices > 1) cluster_sync();
+    }
     return;
   }
   // ------------------------------------------------------------------ data

@@ -1,7 +1,8 @@
 """Kernels whose CTAs write into each other's shared memory, read as source (no GPU needed): a wait that
 gives up in one CTA must not let it go while another may still send to it.  After the cluster's CTAs
-have met first, the warps that meet at its last barrier (all of them, or those of one role: threads
-that have left count as arrived) reach it on every path.
+have met first, the warps that may meet at its last barrier (all of them, or those of one role: threads
+that have left count as arrived) come to it on every path; only a warp that has seen the last of what
+can be sent to it may pass it by.
 """
 import os
 import re
