@@ -600,7 +600,9 @@ int pkm_add_rms_norm_backward(const void *sum, int sum_dtype, const float *weigh
  * (a padded table is called with its own V); target [B] int64; loss, lse, dloss [B] fp32; tensor cores,
  * fp32 accumulation.  A token with a negative target (padding) has loss 0 and adds nothing to the
  * gradients; a target >= V counts as one, and sets *status to PKM_ERR_BAD_INDEX.  A token whose
- * dloss is 0 adds nothing to the gradients either, whatever its x holds.
+ * dloss is 0 adds nothing to the gradients either, whatever its x holds.  A logit of -inf is a power of 0: a
+ * target's makes the loss +inf.  One of +inf makes lse +inf and the loss +inf, or NaN where it is the target's,
+ * and the gradient NaN in that row of dx and in dweight's rows of the target and of such logits; NaN is passed on.
  *
  * pkm_vocab_loss: loss, and lse unless NULL.  pkm_vocab_loss_backward: dx [B, dim] bf16 and dweight [V, dim]
  * (either may be NULL: not computed; grad_dtype PKM_BF16: dweight overwritten; PKM_F32: fp32, added to)

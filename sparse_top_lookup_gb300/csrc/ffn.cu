@@ -538,8 +538,8 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
                 most = fmaxf(fmaxf(most, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
               }
               if constexpr (kEpi == kLoss) {
-                // (nothing but -inf yet: powers of -inf - 0)
-                ref = most == -INFINITY ? 0.0f : most;
+                // (nothing but -inf yet, or +inf: powers against 0)
+                ref = fabsf(most) < INFINITY ? most : 0.0f;
                 sum *= top == -INFINITY ? 1.0f : ex2((top - ref) * kLog2e);
               }
               top = most;
@@ -554,8 +554,10 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               if constexpr (kEpi != kLoss) {
                 if (here) {
                   // (a learnt token's is small: its loss still holds it, the log-sum-exp does not; kExp:
-                  // what belongs here is known with the row's sum)
-                  const float mine = kEpi == kExp ? 0.0f : expm1f(p.loss ? -loss : zt - ref);
+                  // what belongs here is known with the row's sum; beside a logit of +inf it is no number)
+                  const float mine = kEpi == kExp      ? 0.0f
+                                     : ref == INFINITY ? NAN
+                                                       : expm1f(p.loss ? -loss : zt - ref);
 #pragma unroll
                   for (int j = 0; j < 32; ++j)
                     if (gc + j == at) v[j] = mine;

@@ -59,9 +59,12 @@ struct Partial {  // sum exp(v - top) = sum
   float top, sum;
 };
 __device__ __forceinline__ float power(float v, float ref) { return ex2((v - ref) * kLog2e); }
+// What powers are taken against for a maximum of `top`: it itself, or 0 where all logits so far are -inf (powers
+// of 0) or one is +inf (its power, and so the sum, is +inf; inf - inf would be no number).
+__device__ __forceinline__ float reference(float top) { return fabsf(top) < INFINITY ? top : 0.0f; }
 // (a part without a finite logit has top = -inf, and a sum of 0 or NaN)
 __device__ __forceinline__ Partial joined(Partial a, Partial b) {
-  const float top = fmaxf(a.top, b.top), ref = top == -INFINITY ? 0.0f : top;
+  const float top = fmaxf(a.top, b.top), ref = reference(top);
   return {top, (a.top == -INFINITY ? a.sum : a.sum * power(a.top, ref)) +
                    (b.top == -INFINITY ? b.sum : b.sum * power(b.top, ref))};
 }
@@ -120,7 +123,7 @@ one_token_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w,
       if (v0 + r >= V || v0 + r == at) z[r] = -INFINITY;
       top = fmaxf(top, z[r]);
     }
-    const float ref = top == -INFINITY ? 0.0f : top;
+    const float ref = reference(top);
     float s = sum.top == -INFINITY ? sum.sum : sum.sum * power(sum.top, ref);
 #pragma unroll
     for (int r = 0; r < kOneRows; ++r) s += power(z[r], ref);
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
       Partial more = {-INFINITY, 0.0f};
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) more.top = fmaxf(more.top, v[u].x);
-      const float ref = more.top == -INFINITY ? 0.0f : more.top;
+      const float ref = reference(more.top);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u)
         more.sum += kExps || v[u].x == -INFINITY ? v[u].y : v[u].y * power(v[u].x, ref);
@@ -267,14 +270,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
     if (t >= p.V && p.status) atomicExch(p.status, PKM_ERR_BAD_INDEX);
     const float zt = there ? kExps ? p.logit[mine] : logits[w] : -INFINITY;
     // both against one reference
-    float ref = kExps ? p.ref[mine] : fmaxf(sum.top, zt);
-    if (ref == -INFINITY) ref = 0.0f;
+    const float ref = kExps ? p.ref[mine] : reference(fmaxf(sum.top, zt));
     const float rest = kExps || sum.top == -INFINITY ? sum.sum : sum.sum * power(sum.top, ref);
     const float total = rest + power(zt, ref), lse = ref + logf(total);
     float loss = 0.0f, scale = there && p.scaled ? p.dloss[mine] : 0.0f;
-    if (there) loss = zt >= ref ? log1pf(rest * power(ref, zt)) : (ref - zt) + logf(total);
+    if (there) {
+      // (of infinite logits: inf - inf is no number if the target's is one of them, a limit if it is not)
+      if (total == INFINITY)
+        loss = zt == INFINITY ? NAN : INFINITY;
+      else
+        loss = zt >= ref ? log1pf(rest * power(ref, zt)) : (ref - zt) + logf(total);
+    }
     if (kExps) {
-      if (!(rest < 0x1p100f && total < 0x1p100f) && fabsf(sum.top) < INFINITY && ref != sum.top) {
+      // (below the range: a token whose target's logit is -inf, or that has none, has a reference that may lie far
+      // above its logits; a target's own power is 1)
+      if ((total >= 0x1p100f || total < 0x1p-100f) && zt != INFINITY && fabsf(sum.top) < INFINITY &&
+          ref != sum.top) {
         p.ref[mine] = sum.top;
         *p.again = 1;
       }

@@ -1,0 +1,111 @@
+"""The head's product with its cross entropy at the ends of its range: what the calls of pkm_vocab_loss
+agree on there.
+
+Tolerances as in test_gpu_vocab_loss.py.
+"""
+import math
+
+import pytest
+
+from test_gpu_vocab_loss import (F64, HALF, check_loss, errors_of_logits, forward, gradient, inputs,
+                                 loss_bounds, near)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+BIG = 1e25  # bf16; its square overflows fp32
+
+
+def with_infinities(B, dim, V, seed=0):
+    """Inputs, and tokens by what their logits hold.  Column 0 of x is BIG in those tokens and 0 in the
+    others, column 0 of W is +-BIG in three rows; column 1 of x moves all of a token's logits."""
+    x, w, target, dloss = inputs(B, dim, V, seed=seed, absent=0.0)
+    up, down, down2 = V // 3, V // 2, V - 1
+    w[:, 0], x[:, 0] = 0, 0
+    w[:, 1], x[:, 1] = 1, 0
+    keep = (target == up) | (target == down) | (target == down2)
+    target[keep] = 1
+    w[up, 0], w[down, 0], w[down2, 0] = BIG, -BIG, -BIG
+    return x, w, target, dloss, up, down
+
+
+@pytest.mark.parametrize("B,V", [(1, 700), (5, 300), (150, 700), (150, 30000)])
+@pytest.mark.parametrize("kind", ["target", "other", "padding"])
+def test_a_logit_of_plus_infinity(B, V, kind):
+    # inf - inf where it is the target's, the limit where it is another's; in every call
+    x, w, target, dloss, up, _ = with_infinities(B, 64, V)
+    b = B // 2
+    x[b, 0] = BIG
+    target[b] = up if kind == "target" else -1 if kind == "padding" else 0
+    rest = torch.arange(B, device="cuda") != b
+    got = dict(zip(("loss", "lse"), forward(x, w, target)))
+    calls = [got, gradient(x, w, target, dloss, True)]
+    calls.append(gradient(x, w, target, dloss, False, lse=got["lse"]))
+    for c in calls:
+        if "loss" in c:
+            assert c["lse"][b].item() == math.inf
+            want = {"target": math.nan, "other": math.inf, "padding": 0.0}[kind]
+            assert c["loss"][b].item() == want or (math.isnan(want) and bool(c["loss"][b].isnan()))
+            if B > 1:
+                check_loss(x[rest], w, target[rest], (c["loss"][rest], c["lse"][rest]))
+        if "dx" in c:
+            if kind == "padding":
+                assert bool((c["dx"][b] == 0).all()) and bool(torch.isfinite(c["dw"]).all())
+            else:
+                assert bool(c["dx"][b].isnan().all())
+                assert bool(c["dw"][target[b]].isnan().all()) and bool(c["dw"][up].isnan().all())
+                others = torch.ones(V, dtype=torch.bool, device="cuda")
+                others[[up, int(target[b])]] = False
+                assert bool(torch.isfinite(c["dw"][others]).all())
+            assert bool(torch.isfinite(c["dx"][rest]).all())
+
+
+@pytest.mark.parametrize("B,V", [(1, 700), (5, 300), (150, 700), (150, 30000)])
+@pytest.mark.parametrize("move", [0.0, -160.0, 300.0])
+@pytest.mark.parametrize("kind", ["target", "other", "padding"])
+def test_a_logit_of_minus_infinity(B, V, kind, move):
+    # a power of 0: only the loss of such a target is infinite
+    x, w, target, dloss, up, down = with_infinities(B, 64, V, seed=1)
+    w[up, 0] = 0
+    b = B // 2
+    x[b, 0], x[b, 1] = BIG, move
+    target[b] = down if kind == "target" else -1 if kind == "padding" else 0
+    X, W = x.to(F64), w.to(F64)
+    Z = X @ W.T
+    Z[b, [down, V - 1]] = -math.inf
+    lse = torch.logsumexp(Z, 1)
+    # (the logits' own error, and the sums': as loss_bounds, without the infinite ones)
+    finite = torch.ones(V, dtype=torch.bool, device="cuda")
+    finite[[down, V - 1]] = False
+    same = target.clone()
+    same[b] = -1 if kind != "other" else 0
+    e_loss, e_lse = loss_bounds(x, w[finite], same.clamp(max=int(finite.sum()) - 1))[2:]
+    got = dict(zip(("loss", "lse"), forward(x, w, target)))
+    step = gradient(x, w, target, dloss, True)
+    back = gradient(x, w, target, dloss, False, lse=lse.float())
+    for c in (got, step):
+        assert abs(float(c["lse"][b].to(F64) - lse[b])) <= 1.05 * float(e_lse[b])
+        if kind == "target":
+            assert c["loss"][b].item() == math.inf
+        elif kind == "padding":
+            assert c["loss"][b].item() == 0
+        else:
+            assert abs(float(c["loss"][b].to(F64) - (lse[b] - Z[b, 0]))) <= 1.05 * float(e_loss[b])
+    # dz in 64 bits; x's column 0 takes part in dW's column 0 alone, W's in dx's
+    there = target >= 0
+    scale = (dloss.to(F64) * there)[:, None]
+    dz = torch.exp(Z - lse[:, None])
+    ez = errors_of_logits(x * (torch.arange(64, device="cuda") > 0), w)
+    ez += 2.0 ** -20 * (2 + Z.abs().nan_to_num(0, 0, 0) + lse.abs()[:, None])
+    eo = 1.05 * scale * dz * ez
+    dz[torch.arange(B, device="cuda")[there], target[there]] -= 1
+    dz *= scale
+    e = HALF * dz.abs() + eo
+    for c in (step, back):
+        sums = (V + 2) * 2.0 ** -24 * (dz.abs() @ W.abs())
+        checks = [("dx", dz @ W, e @ W.abs() + sums)]
+        sums = (B + 2) * 2.0 ** -24 * (dz.abs().T @ X.abs())
+        checks.append(("dw", dz.T @ X, e.T @ X.abs() + HALF * (dz.abs() + e).T @ X.abs() + sums))
+        for name, want, bound in checks:
+            each = 1.02 * (HALF * want.abs() + (1 + HALF) * bound) + 1e-38
+            near(c[name][:, 1:], want[:, 1:], each[:, 1:], 0, name)
