@@ -427,9 +427,9 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
             if (p.loss) loss = p.loss[row];
         }
       }
-      float scale = 1.0f;
+      float scale = 1.0f, all = 1.0f;
       if constexpr (kEpi == kOut) {
-        if (q.all_scale) scale = *q.all_scale;
+        if (q.all_scale) all = *q.all_scale;
         if (q.row_scale && in) scale = q.row_scale[row];
       }
 
@@ -617,7 +617,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               sums(tc, v);
               if (kEpi == kOut && (q.row_scale || q.all_scale))
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= scale;
+                for (int j = 0; j < 32; ++j) v[j] = v[j] * scale * all;  // (their product may be out of range)
               if (!q.add32) {
                 if (lane == 0) blocks_read<1>();  // (the last may be an fp32 block, two buffers)
                 __syncwarp();

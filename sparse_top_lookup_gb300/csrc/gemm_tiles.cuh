@@ -87,7 +87,7 @@ struct Prod {
   // kOut, splits > 1: K in so many stretches of split_kb slabs (the last may be shorter), whose sums go, in
   // fp32 (add32 2), to out's rows from split * (M rounded up to 32) on
   int splits, split_kb;
-  // kOut: each row is multiplied by its own, or all by one, in fp32; or NULL
+  // kOut: each row is multiplied by its own, then all by one, in fp32; or NULL
   const float *row_scale, *all_scale;
   int tiles;
 };

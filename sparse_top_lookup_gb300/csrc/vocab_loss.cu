@@ -20,7 +20,8 @@
 // loss's epilogue writes E = exp(z - r) in bf16 against a reference r of its own for each token, the
 // target's logit, which is known before, and the sums are known after it: dz = dloss exp(r - lse) E beside
 // the target, whose element the join writes.  That factor takes dloss's place, so nothing passes over E
-// again.  E holds for a row whose sum stays below 2^100; when one of a piece does not (its best logit is 69
+// again; it may be 2^-100 of dloss, so the common factor stays out of it here too, and dx's rows are multiplied
+// by the one and the other.  E holds for a row whose sum stays below 2^100; when one of a piece does not (its best logit is 69
 // above the target's), the join takes that row's maximum for its reference and raises a mark, and two
 // launches that do nothing otherwise (7 us) do the piece again.  8192 x 2048 x 131072: 10.7 ms in two passes,
 // 8.3 so.
@@ -156,6 +157,10 @@ __device__ __forceinline__ void scaled_row(const uint4* x, int vecs, float s, ui
   }
 }
 
+// Where powers are kept, x's copy is multiplied by this beside its factors, which are between 1 and 2^-100 of
+// what they are in two passes: bf16's range is 2^-126 to 2^127.
+constexpr float kLift = 0x1p20f;
+
 // What a piece's dloss are divided by in x's copy: that of its first token (of 32) that has one, if it is of a
 // size that leaves the others in range; else 1.  One warp; the same in every warp.
 __device__ __forceinline__ float common_factor(const int64_t* target, const float* dloss, int B, int V) {
@@ -199,7 +204,7 @@ struct JoinArgs {
   uint4* scaled;
   int scaled_vecs;            // from row to row
   float* row_scale;
-  float* common;              // kLoss: common_factor, for dW
+  float* common;              // common_factor, for dW; kExps: for dx, and over kLift for dW
   // kExp: the reference, the target's logit, and the result, where the targets' elements are still to
   // come
   float* ref;
@@ -243,6 +248,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
         sum = joined(sum, more);
     }
   rows[w][lane] = sum;
+  const float common = p.scaled ? common_factor(p.target, p.dloss, p.B, p.V) : 1.0f;
   if (!kExps && b0 + w < p.B) {
     const int64_t t = p.target[b0 + w];
     if (t >= 0 && t < p.V) {
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
       }
       if (scale != 0.0f) {
         p.exps[mine * p.pitch + t] = __float2bfloat16(expm1f(-loss) * total);
-        scale /= total;
+        scale = scale / common / total;
       }
     }
     if (p.scaled) p.row_scale[mine] = scale, scales[w] = scale;
@@ -300,13 +306,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
   }
   if (!p.scaled) return;
   __syncwarp();
-  float common = 1.0f;
-  if (!kExps) {
-    common = common_factor(p.target, p.dloss, p.B, p.V);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.common = common;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.common[0] = common;
+    if (kExps) p.common[1] = common / kLift;
   }
   if (b0 + w < p.B)
-    scaled_row(p.x + (b0 + w) * p.vecs, p.vecs, scales[w] / common, p.scaled + (b0 + w) * p.scaled_vecs);
+    scaled_row(p.x + (b0 + w) * p.vecs, p.vecs, kExps ? scales[w] * kLift : scales[w] / common,
+               p.scaled + (b0 + w) * p.scaled_vecs);
 }
 
 // Ahead of the backward pass's products: a token's factor (dloss, or 0 where its target is none), its row
@@ -558,7 +564,7 @@ struct Out {
   bool first_columns, last_columns;  // of the pieces that dxs joins
   void* dw;           // fp32 if dw32 > 0 (Prod::add32), or NULL
   int dw32;
-  const float* common;  // that multiplies dW, or NULL
+  const float *dx_common, *common;  // that multiply dx (beside its rows' factors) and dW, or NULL
 };
 // dx = dz W and dW = dz^T xs, dz [n, cols] of `pitch` columns, W's rows those of the columns.
 cudaError_t products(GemmArgs& p, const void* dz, int n, int cols, int64_t pitch, const void* w,
@@ -570,7 +576,7 @@ cudaError_t products(GemmArgs& p, const void* dz, int n, int cols, int64_t pitch
     q = Prod{};
     q.segs = 1;
     q.M = n, q.N = dim, q.K = cols, q.b_mn = 1;
-    q.row_scale = row_scale;
+    q.row_scale = row_scale, q.all_scale = o.dx_common;
     int rows = n;
     if (o.dxs) q.add32 = o.first_columns ? 2 : 1;
     if (o.splits > 1) {
@@ -676,6 +682,7 @@ cudaError_t train_pass(const void* x, const void* weight, const int64_t* target,
   float* ref = reinterpret_cast<float*>(parts + s.parts);
   float *factor = ref + s.rows / 4, *logit = factor + s.rows / 4, *scale = logit + s.rows / 4;
   int* again = reinterpret_cast<int*>(scale + s.rows / 4);
+  float* common = reinterpret_cast<float*>(again + 2);
   cudaError_t e;
   for (int64_t b0 = 0; b0 < B; b0 += s.tokens) {
     const int n = (int)(B - b0 < s.tokens ? B - b0 : s.tokens);
@@ -698,6 +705,7 @@ cudaError_t train_pass(const void* x, const void* weight, const int64_t* target,
     j.logit = logit, j.dloss = dloss + b0, j.row_scale = scale;
     j.exps = reinterpret_cast<__nv_bfloat16*>(exps), j.pitch = s.pitch;
     j.scaled = reinterpret_cast<uint4*>(xs), j.scaled_vecs = pitch16(dim) / 8;
+    j.common = common;
     for (int pass = 0; pass < 2; ++pass) {
       p.prods = 1;
       Prod& q = p.prod[0];
@@ -720,6 +728,7 @@ cudaError_t train_pass(const void* x, const void* weight, const int64_t* target,
     if (s.splits > 1) o.dxs = reinterpret_cast<float*>(dxs);
     o.splits = s.splits, o.first_columns = o.last_columns = true;
     o.dw = dweight, o.dw32 = grad_dtype == PKM_F32;
+    o.dx_common = common, o.common = common + 1;
     if (dweight && s.dw32) o.dw = dws, o.dw32 = b0 ? 1 : 2;
     e = products(p, exps, n, V, s.pitch, weight, xs, dim, scale, o, stream);
     if (e != cudaSuccess) return e;

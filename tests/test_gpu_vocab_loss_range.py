@@ -7,8 +7,8 @@ import math
 
 import pytest
 
-from test_gpu_vocab_loss import (F64, HALF, check_loss, errors_of_logits, forward, gradient, inputs,
-                                 loss_bounds, near)
+from test_gpu_vocab_loss import (F64, HALF, check_gradient, check_loss, errors_of_logits, forward,
+                                 gradient, inputs, loss_bounds, near)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -109,3 +109,51 @@ def test_a_logit_of_minus_infinity(B, V, kind, move):
         for name, want, bound in checks:
             each = 1.02 * (HALF * want.abs() + (1 + HALF) * bound) + 1e-38
             near(c[name][:, 1:], want[:, 1:], each[:, 1:], 0, name)
+
+
+# ------------------------------------------------------------------ weights
+
+
+def far_rows(B, dim, V, seed):
+    """Tokens whose target lies 40 to 65 below their best logit."""
+    x, w, target, _ = inputs(B, dim, V, seed=seed, absent=0.0, sd=7.0, lift=0.0)
+    z = x.to(F64) @ w.to(F64).T
+    gap = z.amax(1, keepdim=True) - z
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    aim = 40 + 25 * torch.rand(B, 1, device="cuda", generator=gen, dtype=F64)
+    target = (gap - aim).abs().argmin(1)
+    at = gap.gather(1, target[:, None])
+    assert float(at.min()) > 35 and float(at.max()) < 67
+    return x, w, target
+
+
+@pytest.mark.parametrize("dim", [64, 200])
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e-8, 1e-10, 1e-12, 1e-16])
+def test_tokens_far_from_their_targets_with_small_weights(size, dim):
+    # a step that keeps powers: rows' factors down to 2^-94 of dloss
+    B = 100
+    x, w, target = far_rows(B, dim, 30000, seed=3)
+    dloss = size * (0.5 + torch.rand(B, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)))
+    check_gradient(x, w, target, dloss)
+
+
+@pytest.mark.parametrize("first", [0.0, 1e-30, 1e30, math.nan])
+def test_tokens_of_very_different_weight_in_a_step_that_keeps_powers(first):
+    x, w, target, dloss = inputs(100, 64, 30000, seed=8, absent=0.0)
+    target[:40] = -1
+    dloss[:40] = first  # (padding: whatever it holds)
+    check_gradient(x, w, target, dloss)
+    if first == 0.0:
+        dloss[50], dloss[60:] = 1e-6, 1e-12
+        check_gradient(x, w, target, dloss)
+        dloss[:] *= 1e-16
+        check_gradient(x, w, target, dloss)
+
+
+def test_one_light_token_far_from_its_target():
+    # its target's row and its best logit's get next to nothing from the others
+    x, w, target = far_rows(100, 64, 30000, seed=5)
+    dloss = torch.full((100,), 1.0, device="cuda")
+    dloss[1:] = 1e-10
+    check_gradient(x, w, target, dloss)
+    check_gradient(x, w, target, dloss.flip(0).contiguous())
