@@ -204,7 +204,7 @@ struct JoinArgs {
   uint4* scaled;
   int scaled_vecs;            // from row to row
   float* row_scale;
-  float* common;              // common_factor, for dW; kExps: for dx, and over kLift for dW
+  float* common;              // common_factor, for dW; kExps: it is there already
   // kExp: the reference, the target's logit, and the result, where the targets' elements are still to
   // come
   float* ref;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
         sum = joined(sum, more);
     }
   rows[w][lane] = sum;
-  const float common = p.scaled ? common_factor(p.target, p.dloss, p.B, p.V) : 1.0f;
+  const float common = kExps ? *p.common : p.scaled ? common_factor(p.target, p.dloss, p.B, p.V) : 1.0f;
   if (!kExps && b0 + w < p.B) {
     const int64_t t = p.target[b0 + w];
     if (t >= 0 && t < p.V) {
@@ -306,10 +306,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
   }
   if (!p.scaled) return;
   __syncwarp();
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.common[0] = common;
-    if (kExps) p.common[1] = common / kLift;
-  }
+  if (!kExps && blockIdx.x == 0 && threadIdx.x == 0) *p.common = common;
   if (b0 + w < p.B)
     scaled_row(p.x + (b0 + w) * p.vecs, p.vecs, kExps ? scales[w] * kLift : scales[w] / common,
                p.scaled + (b0 + w) * p.scaled_vecs);
@@ -336,14 +333,17 @@ rows_kernel(const uint4* __restrict__ x, const int64_t* __restrict__ target,
 }
 
 // Ahead of a training step's products: a token's reference, the target's logit (of column 0 where it has
-// none), and whether it has a gradient.
+// none), and whether it has a gradient; the common factor, for dx, and over kLift for dW.
 __global__ void __launch_bounds__(256)
 reference_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w,
                  const int64_t* __restrict__ target, const float* __restrict__ dloss, int B, int vecs,
-                 int V, float* ref, float* logit, float* factor, int* again) {
+                 int V, float* ref, float* logit, float* factor, int* again, float* common) {
   const int64_t b = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   wait_for_launch_ahead();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *again = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
+    const float all = common_factor(target, dloss, B, V);
+    if (threadIdx.x == 0) *again = 0, common[0] = all, common[1] = all / kLift;
+  }
   if (b >= B) return;
   const int64_t t = target[b];
   const bool there = t >= 0 && t < V;
@@ -689,7 +689,7 @@ cudaError_t train_pass(const void* x, const void* weight, const int64_t* target,
     const uint16_t* xb = static_cast<const uint16_t*>(x) + b0 * dim;
     e = launch_early(reference_kernel, dim3((unsigned)(n + 7) / 8), 256, 0, stream,
                      reinterpret_cast<const uint4*>(xb), static_cast<const uint4*>(weight), target + b0,
-                     dloss + b0, n, dim / 8, V, ref, logit, factor, again);
+                     dloss + b0, n, dim / 8, V, ref, logit, factor, again, common);
     if (e != cudaSuccess) return e;
     GemmArgs p = {};
     p.status = status;
