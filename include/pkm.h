@@ -608,12 +608,17 @@ int pkm_add_rms_norm_backward(const void *sum, int sum_dtype, const float *weigh
  * (either may be NULL: not computed; grad_dtype PKM_BF16: dweight overwritten; PKM_F32: fp32, added to)
  * from the forward's lse and the loss's gradient dloss; z is computed again.  pkm_vocab_loss_train: all of it
  * in one call, for a training step that knows dloss beforehand (1 / B for a mean).  dz is rounded to bf16
- * once, as an operand of the tensor cores, and so is x times its token's factor, where it is not 1.  The backward pass's
- * exp(z - lse) - 1 of a target is good to the roundings of an fp32 lse and of z (some 2^-20 of the logit: a
- * learnt token's own gradient may be smaller than that); the training step's is good relative to itself.
+ * once, as an operand of the tensor cores, and so is x times its token's factor, where it is not 1.
+ *
+ * A target's own exp(z - lse) - 1 is good relative to itself in the training step.  From an lse in fp32 it is
+ * good to 2^-24 of lse (a learnt token's own gradient may be smaller than that; it is 0 then, or has the right
+ * sign): pkm_vocab_loss_backward_with_loss takes the forward's loss beside lse, and has it as the training step
+ * does.  A training step of more than some 76 * 2^16 logits saves a quarter of the products, in which a token's
+ * factor is not 1 even where all dloss are the same; pkm_vocab_loss and pkm_vocab_loss_backward_with_loss, one
+ * after the other, are the same step with all products, and x as it is for a mean.
  *
  * workspace: device scratch of pkm_vocab_loss_workspace_bytes(B, dim, V) bytes, or of
- * pkm_vocab_loss_backward_workspace_bytes(B, dim, V, grad_dtype) for the other two, caller-owned, 16-byte
+ * pkm_vocab_loss_backward_workspace_bytes(B, dim, V, grad_dtype) for the others, caller-owned, 16-byte
  * aligned; it holds nothing between calls.  It holds 1 GiB of dz at most at a time (256 tokens or columns
  * at the least), and beside it what joins the pieces: dx's sums in fp32 where the vocabulary is cut, a bf16
  * dweight's (4 V dim bytes) where the tokens are; a training step takes as much more of dz instead where
@@ -632,6 +637,10 @@ size_t pkm_vocab_loss_backward_workspace_bytes(int B, int dim, int V, int grad_d
 int pkm_vocab_loss_backward(const void *x, const void *weight, const int64_t *target, const float *lse,
                             const float *dloss, int B, int dim, int V, void *workspace, void *dx,
                             void *dweight, int grad_dtype, int *status, void *stream);
+int pkm_vocab_loss_backward_with_loss(const void *x, const void *weight, const int64_t *target,
+                                      const float *lse, const float *loss, const float *dloss, int B,
+                                      int dim, int V, void *workspace, void *dx, void *dweight,
+                                      int grad_dtype, int *status, void *stream);
 int pkm_vocab_loss_train(const void *x, const void *weight, const int64_t *target, const float *dloss,
                          int B, int dim, int V, void *workspace, float *loss, float *lse, void *dx,
                          void *dweight, int grad_dtype, int *status, void *stream);

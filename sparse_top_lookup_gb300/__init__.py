@@ -38,8 +38,8 @@ EXPORTED = ["pkm_create", "pkm_destroy", "pkm_forward", "pkm_lookup", "pkm_gathe
             "pkm_distill_train", "pkm_add_rms_norm", "pkm_add_rms_norm_backward",
             "pkm_add_rms_norm_backward_workspace_bytes", "pkm_usage_balance",
             "pkm_usage_balance_backward", "pkm_usage_balance_workspace_bytes", "pkm_vocab_loss",
-            "pkm_vocab_loss_backward", "pkm_vocab_loss_train", "pkm_vocab_loss_workspace_bytes",
-            "pkm_vocab_loss_backward_workspace_bytes"]
+            "pkm_vocab_loss_backward", "pkm_vocab_loss_backward_with_loss", "pkm_vocab_loss_train",
+            "pkm_vocab_loss_workspace_bytes", "pkm_vocab_loss_backward_workspace_bytes"]
 PKM_STATIC_MAX_PAIRS = 1 << 16
 
 
@@ -124,6 +124,7 @@ def lib():
         L.pkm_usage_balance_backward.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp, vp, vp]
         L.pkm_vocab_loss.argtypes = [vp, vp, vp, i32, i32, i32] + [vp] * 5
         L.pkm_vocab_loss_backward.argtypes = [vp] * 5 + [i32] * 3 + [vp] * 3 + [i32, vp, vp]
+        L.pkm_vocab_loss_backward_with_loss.argtypes = [vp] * 6 + [i32] * 3 + [vp] * 3 + [i32, vp, vp]
         L.pkm_vocab_loss_train.argtypes = [vp] * 4 + [i32] * 3 + [vp] * 5 + [i32, vp, vp]
         L.pkm_vocab_loss_workspace_bytes.argtypes = [i32, i32, i32]
         L.pkm_vocab_loss_workspace_bytes.restype = ctypes.c_size_t
@@ -141,7 +142,8 @@ def lib():
                   "pkm_query_net_batch", "pkm_gated_ffn", "pkm_gated_ffn_backward", "pkm_distill",
                   "pkm_distill_backward", "pkm_distill_train", "pkm_add_rms_norm",
                   "pkm_add_rms_norm_backward", "pkm_usage_balance", "pkm_usage_balance_backward",
-                  "pkm_vocab_loss", "pkm_vocab_loss_backward", "pkm_vocab_loss_train"):
+                  "pkm_vocab_loss", "pkm_vocab_loss_backward", "pkm_vocab_loss_backward_with_loss",
+                  "pkm_vocab_loss_train"):
             getattr(L, f).restype = i32
         _lib = L
     return _lib
@@ -485,6 +487,18 @@ def pkm_vocab_loss_backward(x, weight, target, lse, dloss, B, dim, V, workspace,
                                          _dense(lse, w), _dense(dloss, w), B, dim, V,
                                          _dense(workspace, w), _dense(dx, w), _dense(dweight, w),
                                          grad_dtype, _addr(status), _stream(stream))
+
+
+def pkm_vocab_loss_backward_with_loss(x, weight, target, lse, loss, dloss, B, dim, V, workspace, dx,
+                                      dweight, grad_dtype=PKM_BF16, status=None, stream=None):
+    """As pkm_vocab_loss_backward, from the forward's loss beside its lse: a learnt token's own gradient
+    is good relative to itself."""
+    w = "pkm_vocab_loss_backward_with_loss"
+    return lib().pkm_vocab_loss_backward_with_loss(_dense(x, w), _dense(weight, w), _dense(target, w),
+                                                   _dense(lse, w), _dense(loss, w), _dense(dloss, w), B,
+                                                   dim, V, _dense(workspace, w), _dense(dx, w),
+                                                   _dense(dweight, w), grad_dtype, _addr(status),
+                                                   _stream(stream))
 
 
 def pkm_vocab_loss_train(x, weight, target, dloss, B, dim, V, workspace, loss, lse, dx, dweight,

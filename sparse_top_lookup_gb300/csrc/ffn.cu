@@ -423,8 +423,7 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
           const int64_t t = p.target[row];
           if (t >= p.col0 && t < p.col0 + N) at = (int)(t - p.col0);
           if constexpr (kEpi != kLoss) ref = p.ref[row], live = p.factor[row] != 0.0f;
-          if constexpr (kEpi == kProb)
-            if (p.loss) loss = p.loss[row];
+          if constexpr (kEpi == kProb) loss = p.loss[row];
         }
       }
       float scale = 1.0f, all = 1.0f;
@@ -522,14 +521,10 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : -INFINITY;
               const bool here = __any_sync(0xffffffffu, (unsigned)(at - gc) < 32u);
-              float zt = 0.0f;
-              if (here)
+              if (kEpi != kProb && here)
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (gc + j == at) {
-                    zt = v[j];
-                    if (kEpi != kProb) v[j] = -INFINITY;
-                  }
+                  if (gc + j == at) v[j] = -INFINITY;
               float most = top;
               if constexpr (kEpi != kProb) {
                 float m[4] = {v[0], v[1], v[2], v[3]};
@@ -553,11 +548,9 @@ ffn_gemm_kernel(const __grid_constant__ GemmArgs p) {
               }
               if constexpr (kEpi != kLoss) {
                 if (here) {
-                  // (a learnt token's is small: its loss still holds it, the log-sum-exp does not; kExp:
-                  // what belongs here is known with the row's sum; beside a logit of +inf it is no number)
-                  const float mine = kEpi == kExp      ? 0.0f
-                                     : ref == INFINITY ? NAN
-                                                       : expm1f(p.loss ? -loss : zt - ref);
+                  // (a learnt token's is small: its loss still holds it, this logit and the log-sum-exp do not;
+                  // kExp: what belongs here is known with the row's sum; beside a logit of +inf it is no number)
+                  const float mine = kEpi == kExp ? 0.0f : ref == INFINITY ? NAN : expm1f(-loss);
 #pragma unroll
                   for (int j = 0; j < 32; ++j)
                     if (gc + j == at) v[j] = mine;

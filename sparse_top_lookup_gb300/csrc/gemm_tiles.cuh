@@ -102,7 +102,7 @@ struct GemmArgs {
   int64_t col0;
   float2* row_parts;         // kLoss, kExp: [half a tile][row], maximum and sum
   const float* ref;          // kExp: [row]; kProb: the log-sum-exp
-  const float* loss;         // kProb: [row], or NULL
+  const float* loss;         // kProb: [row]
   const float* factor;       // kProb, kExp: [row], a row of 0 is written as zeros
   const int* only_if;        // NULL, or a word on the device: nothing is done if it is 0
   Plan plan;

@@ -217,16 +217,17 @@ cudaError_t launch_usage_balance_backward(const int64_t* idx, const int* counts,
                                           cudaStream_t stream);
 
 // The head's product and its softmax cross entropy (vocab_loss.cu); arguments as pkm_vocab_loss's,
-// pkm_vocab_loss_backward's and pkm_vocab_loss_train's, checked.
+// pkm_vocab_loss_backward's (loss: NULL, or as pkm_vocab_loss_backward_with_loss's) and pkm_vocab_loss_train's,
+// checked.
 size_t vocab_loss_workspace_bytes(int B, int V);
 size_t vocab_loss_backward_workspace_bytes(int B, int dim, int V, int grad_dtype);
 cudaError_t launch_vocab_loss(const void* x, const void* weight, const int64_t* target, int B, int dim,
                               int V, void* workspace, float* loss, float* lse, int* status,
                               cudaStream_t stream);
 cudaError_t launch_vocab_loss_backward(const void* x, const void* weight, const int64_t* target,
-                                       const float* lse, const float* dloss, int B, int dim, int V,
-                                       void* workspace, void* dx, void* dweight, int grad_dtype,
-                                       int* status, cudaStream_t stream);
+                                       const float* lse, const float* loss, const float* dloss, int B,
+                                       int dim, int V, void* workspace, void* dx, void* dweight,
+                                       int grad_dtype, int* status, cudaStream_t stream);
 cudaError_t launch_vocab_loss_train(const void* x, const void* weight, const int64_t* target,
                                     const float* dloss, int B, int dim, int V, void* workspace,
                                     float* loss, float* lse, void* dx, void* dweight, int grad_dtype,

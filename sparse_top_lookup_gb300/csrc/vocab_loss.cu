@@ -12,7 +12,8 @@
 //
 // Backward: z is computed again, and its epilogue writes dz / dloss = exp(z - lse) - [target] in bf16,
 // piece by piece (of the tokens, and of the vocabulary within), then dx and dW of the piece in one
-// launch; dloss multiplies dx's rows in fp32, and x in dW's operand, over what most tokens' dloss is in a
+// launch; the target's own, exp(-loss) - 1, comes from the forward's loss, or from lse and once more an fp32 sum for
+// its logit, which leaves lse's rounding in it (2^-24 of lse; not less than 0 is left of 1 - exp(-loss)); dloss multiplies dx's rows in fp32, and x in dW's operand, over what most tokens' dloss is in a
 // mean (common_factor, which multiplies dW in fp32): x is rounded once more only where tokens weigh
 // differently.
 //
@@ -313,11 +314,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
 }
 
 // Ahead of the backward pass's products: a token's factor (dloss, or 0 where its target is none), its row
-// of x times that over the common one, and the common one.
+// of x times that over the common one, the common one, and, unless loss is NULL, the token's loss from lse.
 __global__ void __launch_bounds__(256)
-rows_kernel(const uint4* __restrict__ x, const int64_t* __restrict__ target,
-            const float* __restrict__ dloss, int B, int vecs, int V, float* scale, uint4* out,
-            int out_vecs, float* common, int* status) {
+rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w, const int64_t* __restrict__ target,
+            const float* __restrict__ lse, const float* __restrict__ dloss, int B, int vecs, int V,
+            float* scale, float* loss, uint4* out, int out_vecs, float* common, int* status) {
   const int64_t b = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   wait_for_launch_ahead();
   const float all = common_factor(target, dloss, B, V);
@@ -328,6 +329,10 @@ rows_kernel(const uint4* __restrict__ x, const int64_t* __restrict__ target,
   if ((threadIdx.x & 31) == 0) {
     scale[b] = s;
     if (t >= V && status) atomicExch(status, PKM_ERR_BAD_INDEX);
+  }
+  if (loss && t >= 0 && t < V) {
+    const float from_lse = lse[b] - dot_row(x + b * vecs, w + t * vecs, vecs);
+    if ((threadIdx.x & 31) == 0) loss[b] = from_lse < 0.0f ? 0.0f : from_lse;
   }
   scaled_row(x + b * vecs, vecs, s / all, out + b * out_vecs);
 }
@@ -488,8 +493,8 @@ size_t train_region(int B, int dim, int V, int grad_dtype) {
   return s.exps + s.x + s.dxs + s.dws + s.parts + 4 * s.rows + 256;
 }
 
-// The tokens' factors, and the common one.
-size_t scale_region(int B) { return align256((size_t)B * 4 + 4); }
+// The tokens' factors, their losses, and the common factor.
+size_t scale_region(int B) { return align256((size_t)B * 8 + 4); }
 
 size_t gemm_region() { return kPartsBytes + kFlagsBytes; }
 
@@ -615,12 +620,13 @@ cudaError_t products(GemmArgs& p, const void* dz, int n, int cols, int64_t pitch
   return launch_round(o.dxs, o.splits, up(n, 32) * pitch32(dim), n, dim, pitch32(dim), o.dx, stream);
 }
 
-// loss: NULL, or the tokens' losses, whose join has scaled x's rows already
+// loss: NULL, or the tokens' losses; scaled: their join has scaled x's rows already
 cudaError_t gradient_pass(const void* x, const void* weight, const int64_t* target, const float* lse,
-                          const float* loss, const float* dloss, int B, int dim, int V, void* gemm,
-                          unsigned char* region, void* dx, void* dweight, int grad_dtype, int* status, cudaStream_t stream) {
+                          const float* loss, bool scaled, const float* dloss, int B, int dim, int V,
+                          void* gemm, unsigned char* region, void* dx, void* dweight, int grad_dtype,
+                          int* status, cudaStream_t stream) {
   const Pieces s = pieces_of(B, dim, V, grad_dtype);
-  float *scale = reinterpret_cast<float*>(region), *common = scale + B;
+  float *scale = reinterpret_cast<float*>(region), *from_lse = scale + B, *common = from_lse + B;
   unsigned char* dz = region + scale_region(B);
   unsigned char *xs = dz + s.dz, *dxs = xs + s.x, *dws = dxs + s.dxs;
   const uint16_t* w = static_cast<const uint16_t*>(weight);
@@ -628,9 +634,10 @@ cudaError_t gradient_pass(const void* x, const void* weight, const int64_t* targ
   for (int64_t b0 = 0; b0 < B; b0 += s.tokens) {
     const int n = (int)(B - b0 < s.tokens ? B - b0 : s.tokens);
     const uint16_t* xb = static_cast<const uint16_t*>(x) + b0 * dim;
-    if (!loss) {
+    if (!scaled) {
       e = launch_early(rows_kernel, dim3((unsigned)(n + 7) / 8), 256, 0, stream,
-                       reinterpret_cast<const uint4*>(xb), target + b0, dloss + b0, n, dim / 8, V, scale + b0,
+                       reinterpret_cast<const uint4*>(xb), reinterpret_cast<const uint4*>(w), target + b0,
+                       lse + b0, dloss + b0, n, dim / 8, V, scale + b0, loss ? nullptr : from_lse + b0,
                        reinterpret_cast<uint4*>(xs), pitch16(dim) / 8, common, status);
       if (e != cudaSuccess) return e;
     }
@@ -647,7 +654,7 @@ cudaError_t gradient_pass(const void* x, const void* weight, const int64_t* targ
       p.target = target + b0;
       p.col0 = c0;
       p.ref = lse + b0;
-      p.loss = loss;
+      p.loss = (loss ? loss : from_lse) + b0;
       p.factor = scale + b0;
       if (!rows_operand(q, xb, n, dim) || !result(&q.out, dz, n, cols, false, s.pitch))
         return cudaErrorInvalidValue;
@@ -748,11 +755,11 @@ cudaError_t launch_vocab_loss(const void* x, const void* weight, const int64_t* 
 }
 
 cudaError_t launch_vocab_loss_backward(const void* x, const void* weight, const int64_t* target,
-                                       const float* lse, const float* dloss, int B, int dim, int V,
-                                       void* workspace, void* dx, void* dweight, int grad_dtype,
-                                       int* status, cudaStream_t stream) {
+                                       const float* lse, const float* loss, const float* dloss, int B,
+                                       int dim, int V, void* workspace, void* dx, void* dweight,
+                                       int grad_dtype, int* status, cudaStream_t stream) {
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  return gradient_pass(x, weight, target, lse, nullptr, dloss, B, dim, V, ws, ws + gemm_region(), dx,
+  return gradient_pass(x, weight, target, lse, loss, false, dloss, B, dim, V, ws, ws + gemm_region(), dx,
                        dweight, grad_dtype, status, stream);
 }
 
@@ -768,12 +775,12 @@ cudaError_t launch_vocab_loss_train(const void* x, const void* weight, const int
     JoinArgs step = {};
     step.dloss = dloss;
     step.scaled = reinterpret_cast<uint4*>(dz + s.dz), step.scaled_vecs = pitch16(dim) / 8;
-    step.row_scale = reinterpret_cast<float*>(region), step.common = step.row_scale + B;
+    step.row_scale = reinterpret_cast<float*>(region), step.common = step.row_scale + 2 * (size_t)B;
     cudaError_t e = loss_pass(x, weight, target, B, dim, V, ws, dz + s.dz + s.x, loss, lse, status, &step,
                               stream);
     if (e != cudaSuccess) return e;
-    return gradient_pass(x, weight, target, lse, loss, dloss, B, dim, V, ws, region, dx, dweight, grad_dtype,
-                         status, stream);
+    return gradient_pass(x, weight, target, lse, loss, true, dloss, B, dim, V, ws, region, dx, dweight,
+                         grad_dtype, status, stream);
   }
   return train_pass(x, weight, target, dloss, B, dim, V, ws, ws + gemm_region(), loss, lse, dx, dweight,
                     grad_dtype, status, stream);
@@ -839,22 +846,43 @@ extern "C" int pkm_vocab_loss(const void* x, const void* weight, const int64_t* 
                                          static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" int pkm_vocab_loss_backward(const void* x, const void* weight, const int64_t* target,
-                                       const float* lse, const float* dloss, int B, int dim, int V,
-                                       void* workspace, void* dx, void* dweight, int grad_dtype,
-                                       int* status, void* stream) {
+namespace {
+
+// loss: of the second call, which needs it
+int vocab_backward(const void* x, const void* weight, const int64_t* target, const float* lse,
+                   bool with_loss, const float* loss, const float* dloss, int B, int dim, int V,
+                   void* workspace, void* dx, void* dweight, int grad_dtype, int* status, void* stream) {
   int rc = vocab_check(B, dim, V);
   if (rc) return rc;
   if (grad_dtype != PKM_BF16 && grad_dtype != PKM_F32) return PKM_ERR_UNSUPPORTED;
   if (B == 0) return vocab_empty(dim, V, dweight, grad_dtype, stream);
-  if (!lse || !dloss) return PKM_ERR_INVALID;
+  if (!lse || !dloss || (with_loss && !loss)) return PKM_ERR_INVALID;
   if ((rc = vocab_inputs(x, weight, target, workspace, status))) return rc;
-  if (!vocab_aligned(lse, 4) || !vocab_aligned(dloss, 4) || !vocab_aligned(dx, 16) ||
-      !vocab_aligned(dweight, 16))
+  if (!vocab_aligned(lse, 4) || !vocab_aligned(loss, 4) || !vocab_aligned(dloss, 4) ||
+      !vocab_aligned(dx, 16) || !vocab_aligned(dweight, 16))
     return PKM_ERR_ALIGN;
-  return vocab_rc(pkm::launch_vocab_loss_backward(x, weight, target, lse, dloss, B, dim, V, workspace, dx,
-                                                  dweight, grad_dtype, status,
+  return vocab_rc(pkm::launch_vocab_loss_backward(x, weight, target, lse, loss, dloss, B, dim, V,
+                                                  workspace, dx, dweight, grad_dtype, status,
                                                   static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" int pkm_vocab_loss_backward(const void* x, const void* weight, const int64_t* target,
+                                       const float* lse, const float* dloss, int B, int dim, int V,
+                                       void* workspace, void* dx, void* dweight, int grad_dtype,
+                                       int* status, void* stream) {
+  return vocab_backward(x, weight, target, lse, false, nullptr, dloss, B, dim, V, workspace, dx, dweight,
+                        grad_dtype, status, stream);
+}
+
+extern "C" int pkm_vocab_loss_backward_with_loss(const void* x, const void* weight,
+                                                 const int64_t* target, const float* lse,
+                                                 const float* loss, const float* dloss, int B, int dim,
+                                                 int V, void* workspace, void* dx, void* dweight,
+                                                 int grad_dtype, int* status, void* stream) {
+  return vocab_backward(x, weight, target, lse, true, loss, dloss, B, dim, V, workspace, dx, dweight,
+                        grad_dtype, status, stream);
 }
 
 extern "C" int pkm_vocab_loss_train(const void* x, const void* weight, const int64_t* target,

@@ -7,8 +7,10 @@ import math
 
 import pytest
 
-from test_gpu_vocab_loss import (F64, HALF, check_gradient, check_loss, errors_of_logits, forward,
-                                 gradient, inputs, loss_bounds, near)
+import sparse_top_lookup_gb300 as pk
+from more_operators64 import Guarded, vocab64
+from test_gpu_vocab_loss import (BF16, F64, HALF, check_gradient, check_loss, errors_of_logits,
+                                 forward, gradient, inputs, loss_bounds, near)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -157,3 +159,125 @@ def test_one_light_token_far_from_its_target():
     dloss[1:] = 1e-10
     check_gradient(x, w, target, dloss)
     check_gradient(x, w, target, dloss.flip(0).contiguous())
+
+
+# ------------------------------------------------------------------ learnt tokens
+
+
+def learnt(dim, V, far, move, seed):
+    """One token, some `far` ahead in its target's logit, which is a sum of terms of either sign; all
+    logits are moved by `move`."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    w = (torch.randn(V, dim, device="cuda", generator=gen) * 0.05).to(BF16)
+    target = torch.tensor([V // 2], device="cuda")
+    w[target] = torch.randn(1, dim, device="cuda", generator=gen).to(BF16)
+    x = torch.randn(1, dim, device="cuda", generator=gen)
+    t = w[target].float()
+    x += t * (far - (x * t).sum()) / t.square().sum()
+    x[:, 0], w[:, 0] = move, 1
+    return x.to(BF16), w, target, torch.ones(1, device="cuda")
+
+
+def with_loss(x, w, target, lse, loss, dloss, grad_dtype=pk.PKM_BF16, status=None, stream=None):
+    (B, dim), V = x.shape, w.shape[0]
+    f32 = grad_dtype == pk.PKM_F32
+    dx = Guarded(B, dim, dtype=BF16)
+    dw = Guarded(V, dim, dtype=torch.float32, fill=3.0) if f32 else Guarded(V, dim, dtype=BF16)
+    ws = Guarded(pk.pkm_vocab_loss_backward_workspace_bytes(B, dim, V, grad_dtype), dtype=torch.uint8,
+                 fill=255)
+    pk.check(pk.pkm_vocab_loss_backward_with_loss(x, w, target, lse, loss, dloss, B, dim, V, ws.t, dx.t,
+                                                  dw.t, grad_dtype, status, stream), "backward")
+    torch.cuda.synchronize()
+    assert dx.ok() and dw.ok() and ws.ok()
+    return {"dx": dx.t, "dw": dw.t}
+
+
+@pytest.mark.parametrize("dim", [64, 512, 2048])
+@pytest.mark.parametrize("V", [500, 40000])
+@pytest.mark.parametrize("move", [0, -100])
+def test_a_learnt_tokens_gradient(V, dim, move):
+    # from lse: off by the lse's rounding and the logit's fp32 sum, and never the other way; with the
+    # loss: by three roundings of its own size
+    for i, far in enumerate(range(10, 60, 3)):
+        x, w, target, dloss = learnt(dim, V, far, move, seed=i)
+        X, W = x.to(F64), w.to(F64)
+        loss64, lse64, dz = vocab64(X, W, target, dloss.to(F64))
+        want = dz[0, target[0]] * X[0]
+        sizes = (X[0].abs() * W[target[0]].abs()).sum()
+        got = gradient(x, w, target, dloss, False, lse=lse64.float())["dw"][target[0]].to(F64)
+        assert bool((got * X[0] <= 0).all()), far
+        # a lane's sum of dim / 32 products and five additions; lse and its difference are rounded
+        e = (dim / 32 + 6) * 2.0 ** -24 * sizes + 2 * 2.0 ** -24 * lse64.abs()
+        each = 1.01 * (3 * HALF * want.abs() + e * X[0].abs()) + 1e-38
+        off = (got - want).abs()
+        assert bool((off <= each).all()), (far, float((off - each).max()))
+        # the forward's own loss, good to its bound
+        loss, lse = forward(x, w, target)
+        got = with_loss(x, w, target, lse, loss, dloss)["dw"][target[0]].to(F64)
+        e = loss_bounds(x, w, target)[2] / loss64 + 2.0 ** -20
+        assert bool(((got - want).abs() <= 1.01 * (3 * HALF + e) * want.abs() + 1e-38).all()), far
+
+
+@pytest.mark.parametrize("B,dim,V", [(1, 64, 40000), (130, 136, 4099), (257, 264, 513), (1001, 520, 3001),
+                                     (33000, 16, 300), (20, 264, 50257)])
+def test_the_forward_and_the_backward_pass_with_its_loss(B, dim, V):
+    # are the step that forms all products
+    x, w, target, dloss = inputs(B, dim, V, seed=V)
+    loss, lse = forward(x, w, target)
+    X, W = x.to(F64), w.to(F64)
+    _, _, dz = vocab64(X, W, target, dloss.to(F64))
+    e_loss, e_lse = loss_bounds(x, w, target)[2:]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = with_loss(x, w, target, lse, loss, dloss, status=status)
+    assert status.item() == pk.PKM_OK
+    eo = 1.05 * (dz.abs() * (errors_of_logits(x, w) + e_lse[:, None] + 2.0 ** -20 * (1 + lse.to(F64).abs()[:, None])))
+    there = target >= 0
+    at = target.clamp(min=0)[:, None]
+    mine = 1.05 * (dloss.to(F64) * there * (e_loss + 2.0 ** -22))[:, None]
+    eo = eo.scatter(1, at, mine)
+    e = HALF * dz.abs() + eo
+    sums = (V + 2) * 2.0 ** -24 * (dz.abs() @ W.abs())
+    want = dz @ W
+    near(got["dx"], want, 1.01 * (HALF * want.abs() + (1 + HALF) * (e @ W.abs() + sums)) + 1e-38, 2, "dx",
+         eo @ W.abs() + sums)
+    sums = (B + 2) * 2.0 ** -24 * (dz.abs().T @ X.abs())
+    want = dz.T @ X
+    bound = e.T @ X.abs() + sums + 1.01 * HALF * ((dz.abs() + e).T @ X.abs())
+    near(got["dw"], want, 1.01 * (HALF * want.abs() + (1 + HALF) * bound) + 1e-38, 3, "dw",
+         eo.T @ X.abs() + sums)
+    added = with_loss(x, w, target, lse, loss, dloss, pk.PKM_F32)
+    assert torch.equal(added["dx"], got["dx"])
+    near(added["dw"].to(F64) - 3.0, want, 1.01 * bound + 2.0 ** -23 * (3 + want.abs()), 0, "dw")
+    if -(-B // 256) * -(-V // 256) <= 76:  # (one round of tiles: the training step does the same)
+        step = gradient(x, w, target, dloss, True)
+        assert torch.equal(step["loss"], loss) and torch.equal(step["lse"], lse)
+        assert torch.equal(step["dx"], got["dx"]) and torch.equal(step["dw"], got["dw"])
+
+
+def test_the_backward_pass_with_its_loss_on_another_stream_and_in_a_graph():
+    x, w, target, dloss = inputs(300, 136, 5001, seed=2)
+    B, dim, V = 300, 136, 5001
+    target[7] = V  # (counts for nothing, and is reported)
+    loss, lse = forward(x, w, target, status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = with_loss(x, w, target, lse, loss, dloss, status=status)
+    assert status.item() == pk.PKM_ERR_BAD_INDEX and bool((want["dx"][7] == 0).all())
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        got = with_loss(x, w, target, lse, loss, dloss)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    out = {n: torch.empty_like(t) for n, t in want.items()}
+    ws = torch.full((pk.pkm_vocab_loss_backward_workspace_bytes(B, dim, V),), 255, dtype=torch.uint8,
+                    device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        pk.check(pk.pkm_vocab_loss_backward_with_loss(x, w, target, lse, loss, dloss, B, dim, V, ws,
+                                                      out["dx"], out["dw"]), "backward")
+    for _ in range(2):
+        for t in out.values():
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[n], want[n]) for n in want)
