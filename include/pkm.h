@@ -562,8 +562,10 @@ int pkm_distill_train(const void *logits, int logit_dtype, int64_t ld, int B, in
  * and sum does not), or PKM_FP8_E4M3: one buffer in the layout of an fp8 value table, B * dim codes and
  * then B fp32 row scales, with pkm_quantize_values_fp8's recipe.  rstd: NULL, or [B] fp32 for the
  * backward pass.  fp32 between the loads and the one rounding of each result; y comes from the unrounded
- * s.  A row's NaN or infinity stays in its row; sums of squares past fp32's range (|s| of 10^18 and
- * more) make rstd 0.
+ * s.  A row's NaN or infinity stays in its row.  Rows of every size have their norm: where the squares leave fp32's
+ * range (|s| of 10^18 and more, or below some 10^-15 with as small an eps), they are summed of the scaled row.
+ * rstd itself is past fp32's range, and inf, where a row of denormals meets an eps of 0; y holds there too.
+ * A row of zeros with eps 0 has no norm: rstd is inf and y NaN.
  *
  * pkm_add_rms_norm_backward: from the forward's sum and rstd, dy [B, dim] of dy_dtype, and dsum
  * [B, dim] of sum_dtype (what reaches s on other ways; NULL: nothing):

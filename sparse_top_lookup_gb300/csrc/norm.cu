@@ -105,8 +105,115 @@ __device__ __forceinline__ float join_group(float v, int warps, int g, float* sc
 
 constexpr int kNormThreads = 512;  // of a block at most: see shape_of
 
+__device__ __forceinline__ float scale_of(float amax) {
+  const float scale = __fdiv_rn(amax, 448.0f);
+  return scale >= FLT_MIN ? scale : FLT_MIN;
+}
+__device__ __forceinline__ uint2 codes_of(const float (&v)[kVec], float scale) {
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    w[j] = 0;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      w[j] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(v[4 * j + m], scale), __NV_SATFINITE, __NV_E4M3)
+              << (8 * m);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A row whose mean of squares (and eps) lies below this, or past fp32, is summed scaled.  Squares below 2^-126
+// have lost bits, of 16384 of them 2^-136 in the sum at most: this keeps 2^-36 of it clear.
+constexpr float kLeastMean = 0x1p-100f;
+
+struct NormArgs {
+  const float* weight;
+  float eps;
+  int B, dim, warps;
+  void* sum;
+  int sum_dtype;
+  void* y;
+  int y_dtype;
+  float* rstd;
+};
+
+// Row b of such a kind, by its group: s is scaled by a power of two, which brings the largest of it and of
+// sqrt(eps) to 1, and read again each time (from registers these lines would cost the kernel, in all its rows, 8
+// more of them).
+template <typename X, typename R>
+__device__ __noinline__ void scaled_norm_row(const X* x, const R* r, const NormArgs p, int64_t b, int g,
+                                             float (*scratch)[kNormMaxWarps][kNormMaxWarps]) {
+  const int t = threadIdx.x - g * 32 * p.warps, per = 32 * p.warps * kVec;
+  const int64_t row = b * p.dim;
+  auto load = [&](int c, float (&s)[kVec]) {
+    load8(x + row + c, s);
+    if (r) {
+      float v[kVec];
+      load8(r + row + c, v);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) s[j] += v[j];
+    }
+  };
+  float most = 0.0f;
+  for (int c = t * kVec; c < p.dim; c += per) {
+    float s[kVec];
+    load(c, s);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) most = fmaxf(most, fabsf(s[j]));
+  }
+  most = fmaxf(join_group<Max>(most, p.warps, g, scratch[1][g]), __fsqrt_rn(p.eps));
+  float pre = 1.0f;
+  if (most > 0.0f && most < INFINITY) {  // (zeros without eps and infinities have no scale)
+    const int e = min(max((int)(__float_as_uint(most) >> 23) - 127, -126), 126);
+    pre = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+  }
+  float ss = 0.0f;
+  for (int c = t * kVec; c < p.dim; c += per) {
+    float s[kVec];
+    load(c, s);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) ss = fmaf(s[j] * pre, s[j] * pre, ss);
+  }
+  ss = join_group<Sum>(ss, p.warps, g, scratch[0][g]);
+  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)p.dim) + p.eps * pre * pre));
+  if (p.rstd && t == 0) p.rstd[b] = rstd * pre;
+  auto norm = [&](int c, const float (&s)[kVec], float (&v)[kVec]) {
+    load8(p.weight + c, v);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) v[j] = s[j] * pre * (rstd * v[j]);
+  };
+  float scale = 0.0f;
+  if (p.y_dtype == PKM_FP8_E4M3) {
+    float amax = 0.0f;
+    for (int c = t * kVec; c < p.dim; c += per) {
+      float s[kVec], v[kVec];
+      load(c, s);
+      norm(c, s, v);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    }
+    scale = scale_of(join_group<Max>(amax, p.warps, g, scratch[1][g]));
+    if (t == 0) reinterpret_cast<float*>(static_cast<uint8_t*>(p.y) + (int64_t)p.B * p.dim)[b] = scale;
+  }
+  for (int c = t * kVec; c < p.dim; c += per) {  // (a place is read before it is written: sum and y in place)
+    float s[kVec], v[kVec];
+    load(c, s);
+    norm(c, s, v);
+    if (p.sum) store8(p.sum, p.sum_dtype, row + c, s);
+    if (p.y_dtype == PKM_FP8_E4M3)
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + row + c) = codes_of(v, scale);
+    else
+      store8(p.y, p.y_dtype, row + c, v);
+  }
+}
+
+// Rows of 16 bits are bound by what is on its way: three blocks of an SM (40 registers; 16384 x 2048 40.6 us, two
+// blocks 45.6), two of the longest (64; 4096 x 16384 79.5 us, one block 106).  0: as they come.
 template <typename X, typename R, int kN>
-__global__ void __launch_bounds__(kNormThreads)
+constexpr int kNormBlocks = sizeof(X) + sizeof(R) > 4 ? 0 : kN == 2 ? 3 : 2;
+
+template <typename X, typename R, int kN>
+__global__ void __launch_bounds__(kNormThreads, (kNormBlocks<X, R, kN>))
 add_norm_kernel(const X* x, const R* r, const float* __restrict__ weight, float eps, int B, int dim,
                 int warps, void* sum, int sum_dtype, void* y, int y_dtype, float* rstd_out) {
   __shared__ float scratch[2][kNormMaxWarps][kNormMaxWarps];
@@ -144,7 +251,13 @@ add_norm_kernel(const X* x, const R* r, const float* __restrict__ weight, float 
     }
   }
   ss = join_group<Sum>(ss, warps, g, scratch[0][g]);
-  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)dim) + eps));
+  const float mean = __fdiv_rn(ss, (float)dim) + eps;
+  if (!(mean >= kLeastMean && mean < INFINITY)) {  // (the same in all of a row's threads)
+    scaled_norm_row(x, r, NormArgs{weight, eps, B, dim, warps, sum, sum_dtype, y, y_dtype, rstd_out}, b, g,
+                    scratch);
+    return;
+  }
+  const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(mean));
   if (rstd_out && t == 0) rstd_out[b] = rstd;
   float amax = 0.0f;
 #pragma unroll
@@ -164,26 +277,13 @@ add_norm_kernel(const X* x, const R* r, const float* __restrict__ weight, float 
   }
   if (y_dtype != PKM_FP8_E4M3) return;
   amax = join_group<Max>(amax, warps, g, scratch[1][g]);
-  float scale = __fdiv_rn(amax, 448.0f);
-  if (!(scale >= FLT_MIN)) scale = FLT_MIN;
+  const float scale = scale_of(amax);
   uint8_t* codes = static_cast<uint8_t*>(y);
   if (t == 0) reinterpret_cast<float*>(codes + (int64_t)B * dim)[b] = scale;
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
     const int c = i * per + t * kVec;
-    if (c < dim) {
-      uint32_t w[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        w[j] = 0;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          w[j] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(s[i][4 * j + m], scale), __NV_SATFINITE,
-                                                  __NV_E4M3)
-                  << (8 * m);
-      }
-      *reinterpret_cast<uint2*>(codes + row + c) = make_uint2(w[0], w[1]);
-    }
+    if (c < dim) *reinterpret_cast<uint2*>(codes + row + c) = codes_of(s[i], scale);
   }
 }
 
