@@ -421,6 +421,7 @@ Shape shape_of(int dim, int threads) {
 // Blocks of the backward pass, and their parts of dweight: one to an SM (two of 256 threads 50 us at
 // 16384 x 2048, three 61, this 48).
 constexpr int kBackThreads = 512, kMaxParts = 152;
+constexpr int kMostRowBytes = PKM_NORM_MAX_DIM * 4;  // of its dynamic shared memory
 
 template <typename F>
 cudaError_t with_type(int dtype, F&& f) {
@@ -476,8 +477,10 @@ cudaError_t launch_add_rms_norm_backward(const void* sum, int sum_dtype, const f
         using Y = std::remove_pointer_t<decltype(yt)>;
         auto kernel = add_norm_backward_kernel<S, Y, decltype(n)::value>;
         if (smem > kSharedUnasked) {
+          // (the most of any width: what is granted is the kernel's, not this call's, and a narrower call on
+          // another host thread may come between here and the launch)
           cudaError_t e2 = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                (int)smem);
+                                                kMostRowBytes);
           if (e2 != cudaSuccess) return e2;
         }
         return launch_early(kernel, dim3((unsigned)blocks), s.threads, smem, stream, static_cast<const S*>(sum), weight,
