@@ -378,12 +378,16 @@ gather_bulk_kernel(const unsigned char* __restrict__ values, const float* __rest
   __syncthreads();
 }
 
+// Dynamic shared memory of any launch of the two forms.  The most is asked for, whatever a call takes: the grant is
+// the kernel's, and a smaller call on another host thread may come between asking and launching.
+constexpr size_t kBulkMostShared = 220 * 1024, kMostShared = 227 * 1024;
+
 // Shape of the bulk form for a row of vpr 16-byte vectors: the most teams
 // (a power of two) whose staging and two batch slots each fit, or false when
 // the row does not suit it (teams must be whole warps).
 bool bulk_shape(int vpr, int rows_per_bag, int& teams, int& nbs, size_t& smem) {
   if (vpr % 32 || vpr > kBulkConsumers || rows_per_bag < 1) return false;
-  const size_t budget = 220u * 1024u;
+  const size_t budget = kBulkMostShared;
   const size_t per_batch = kBatch * ((size_t)vpr * 16 + 4) + 8 * 2 + 4;
   int tm = 1;
   while (tm * 2 <= kBulkMaxTeams && tm * 2 * vpr <= kBulkConsumers &&
@@ -413,12 +417,12 @@ cudaError_t launch_gather_vt(const void* values, int64_t N, int d_v, int B, int 
   int teams = 0, nbs = 0;
   size_t bulk_smem = 0;
   if (ctas > 0 && bulk_shape(vpr, rows_per_bag, teams, nbs, bulk_smem)) {
-    static size_t smem_set = 0;
-    if (bulk_smem > smem_set) {
+    static bool smem_set = false;
+    if (!smem_set) {
       cudaError_t e = cudaFuncSetAttribute(
-          gather_bulk_kernel<VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bulk_smem);
+          gather_bulk_kernel<VT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBulkMostShared);
       if (e != cudaSuccess) return e;
-      smem_set = bulk_smem;
+      smem_set = true;
     }
     const int64_t want = ((int64_t)B + teams - 1) / teams;
     const int grid = want < ctas ? (int)want : ctas;
@@ -435,7 +439,8 @@ cudaError_t launch_gather_vt(const void* values, int64_t N, int d_v, int B, int 
   const size_t smem = groups > 1 ? red_off + (size_t)threads * E * 4 : staged;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(gather_kernel<VT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kMostShared);
     if (e != cudaSuccess) return e;
   }
   // The loads bypass L1, so the SM can keep its maximum shared-memory split.

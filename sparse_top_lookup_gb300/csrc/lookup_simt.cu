@@ -176,7 +176,7 @@ lookup_simt_kernel(const TIn* __restrict__ q, const TIn* __restrict__ subkeys, i
   lookup_pair(q, subkeys, H, d_q, n, k, (int64_t)blockIdx.x, idx, w, smem);
 }
 
-size_t simt_smem(int d_q, int n_keys, int k) {
+constexpr size_t simt_smem(int d_q, int n_keys, int k) {
   return (size_t)d_q * 4 + (size_t)2 * n_keys * 4 + (size_t)4 * k * 4 + (size_t)2 * k * k * 4 +
          (size_t)2 * k * 4 + 16;
 }
@@ -189,8 +189,11 @@ cudaError_t launch_simt(const TIn* q, const TIn* subkeys, int B, int H, int d_q,
   if (B == 0) return cudaSuccess;
   const size_t smem = simt_smem(d_q, n_keys, k);
   if (smem > 48 * 1024) {
+    // (the most of any call: the grant is the kernel's, and a smaller call on another host thread may come
+    // between here and the launch)
+    constexpr size_t most = simt_smem(kSimtMaxDq, kSimtMaxNKeys, kSimtMaxK);
     cudaError_t e = cudaFuncSetAttribute(lookup_simt_kernel<TIn>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   const int64_t pairs = (int64_t)B * H;
