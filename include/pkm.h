@@ -612,9 +612,9 @@ int pkm_add_rms_norm_backward(const void *sum, int sum_dtype, const float *weigh
  * in one call, for a training step that knows dloss beforehand (1 / B for a mean).  dz is rounded to bf16
  * once, as an operand of the tensor cores, and so is x times its token's factor, where it is not 1.
  *
- * A target's own exp(z - lse) - 1 is good relative to itself in the training step.  From an lse in fp32 it is
- * good to 2^-24 of lse (a learnt token's own gradient may be smaller than that; it is 0 then, or has the right
- * sign): pkm_vocab_loss_backward_with_loss takes the forward's loss beside lse, and has it as the training step
+ * A target's own exp(z - lse) - 1 is good relative to itself in the training step.  From lse alone it is off by
+ * what lse is (by its rounding, 2^-24 of it, at the least: a learnt token's own gradient may be smaller than
+ * that): pkm_vocab_loss_backward_with_loss takes the forward's loss beside lse, and has it as the training step
  * does.  A training step of more than some 76 * 2^16 logits saves a quarter of the products, in which a token's
  * factor is not 1 even where all dloss are the same; pkm_vocab_loss and pkm_vocab_loss_backward_with_loss, one
  * after the other, are the same step with all products, and x as it is for a mean.

@@ -13,7 +13,7 @@
 // Backward: z is computed again, and its epilogue writes dz / dloss = exp(z - lse) - [target] in bf16,
 // piece by piece (of the tokens, and of the vocabulary within), then dx and dW of the piece in one
 // launch; the target's own, exp(-loss) - 1, comes from the forward's loss, or from lse and once more an fp32 sum for
-// its logit, which leaves lse's rounding in it (2^-24 of lse; not less than 0 is left of 1 - exp(-loss)); dloss multiplies dx's rows in fp32, and x in dW's operand, over what most tokens' dloss is in a
+// its logit, which leaves in it what lse is off by (2^-24 of it from its rounding alone); dloss multiplies dx's rows in fp32, and x in dW's operand, over what most tokens' dloss is in a
 // mean (common_factor, which multiplies dW in fp32): x is rounded once more only where tokens weigh
 // differently.
 //
@@ -331,8 +331,9 @@ rows_kernel(const uint4* __restrict__ x, const uint4* __restrict__ w, const int6
     if (t >= V && status) atomicExch(status, PKM_ERR_BAD_INDEX);
   }
   if (loss && t >= 0 && t < V) {
-    const float from_lse = lse[b] - dot_row(x + b * vecs, w + t * vecs, vecs);
-    if ((threadIdx.x & 31) == 0) loss[b] = from_lse < 0.0f ? 0.0f : from_lse;
+    // (below 0 where lse is that of other logits, rounded ones for instance: exp(z - lse) - 1 all the same)
+    const float z = dot_row(x + b * vecs, w + t * vecs, vecs);
+    if ((threadIdx.x & 31) == 0) loss[b] = lse[b] - z;
   }
   scaled_row(x + b * vecs, vecs, s / all, out + b * out_vecs);
 }

@@ -196,8 +196,8 @@ def with_loss(x, w, target, lse, loss, dloss, grad_dtype=pk.PKM_BF16, status=Non
 @pytest.mark.parametrize("V", [500, 40000])
 @pytest.mark.parametrize("move", [0, -100])
 def test_a_learnt_tokens_gradient(V, dim, move):
-    # from lse: off by the lse's rounding and the logit's fp32 sum, and never the other way; with the
-    # loss: by three roundings of its own size
+    # from lse: off by the lse's rounding and the logit's fp32 sum; with the loss: by three roundings of
+    # its own size
     for i, far in enumerate(range(10, 60, 3)):
         x, w, target, dloss = learnt(dim, V, far, move, seed=i)
         X, W = x.to(F64), w.to(F64)
@@ -205,7 +205,6 @@ def test_a_learnt_tokens_gradient(V, dim, move):
         want = dz[0, target[0]] * X[0]
         sizes = (X[0].abs() * W[target[0]].abs()).sum()
         got = gradient(x, w, target, dloss, False, lse=lse64.float())["dw"][target[0]].to(F64)
-        assert bool((got * X[0] <= 0).all()), far
         # a lane's sum of dim / 32 products and five additions; lse and its difference are rounded
         e = (dim / 32 + 6) * 2.0 ** -24 * sizes + 2 * 2.0 ** -24 * lse64.abs()
         each = 1.01 * (3 * HALF * want.abs() + e * X[0].abs()) + 1e-38
@@ -216,6 +215,36 @@ def test_a_learnt_tokens_gradient(V, dim, move):
         got = with_loss(x, w, target, lse, loss, dloss)["dw"][target[0]].to(F64)
         e = loss_bounds(x, w, target)[2] / loss64 + 2.0 ** -20
         assert bool(((got - want).abs() <= 1.01 * (3 * HALF + e) * want.abs() + 1e-38).all()), far
+
+
+@pytest.mark.parametrize("V", [500, 40000])
+@pytest.mark.parametrize("off", [-0.03, 0.03, -3.0])
+def test_the_backward_pass_from_an_lse_of_other_logits(off, V):
+    # exp(z - lse) - [target] of the lse it is given, which may be above 0 at a target
+    B, dim = 150, 128
+    x, w, target, dloss = inputs(B, dim, V, seed=6, lift=14.0)
+    X, W = x.to(F64), w.to(F64)
+    Z = X @ W.T
+    lse = (torch.logsumexp(Z, 1) + off).float()
+    got = gradient(x, w, target, dloss, False, lse=lse)
+    there = target >= 0
+    scale = (dloss.to(F64) * there)[:, None]
+    p = torch.exp(Z - lse.to(F64)[:, None])
+    dz = p.scatter_add(1, target.clamp(min=0)[:, None], -torch.ones(B, 1, dtype=F64, device="cuda")) * scale
+    if off < 0:
+        at = dz.gather(1, target.clamp(min=0)[:, None])[there]
+        assert bool((at > 0).any())
+    eo = 1.05 * scale * p * (errors_of_logits(x, w) + 2.0 ** -20 * (1 + lse.to(F64).abs()[:, None] + Z.abs()))
+    e = HALF * dz.abs() + eo
+    sums = (V + 2) * 2.0 ** -24 * (dz.abs() @ W.abs())
+    want = dz @ W
+    near(got["dx"], want, 1.01 * (HALF * want.abs() + (1 + HALF) * (e @ W.abs() + sums)) + 1e-38, 2, "dx",
+         eo @ W.abs() + sums)
+    sums = (B + 2) * 2.0 ** -24 * (dz.abs().T @ X.abs())
+    want = dz.T @ X
+    bound = e.T @ X.abs() + sums + 1.01 * HALF * ((dz.abs() + e).T @ X.abs())
+    near(got["dw"], want, 1.01 * (HALF * want.abs() + (1 + HALF) * bound) + 1e-38, 3, "dw",
+         eo.T @ X.abs() + sums)
 
 
 @pytest.mark.parametrize("B,dim,V", [(1, 64, 40000), (130, 136, 4099), (257, 264, 513), (1001, 520, 3001),
