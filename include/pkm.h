@@ -616,7 +616,8 @@ int pkm_add_rms_norm_backward(const void *sum, int sum_dtype, const float *weigh
  * what lse is (by its rounding, 2^-24 of it, at the least: a learnt token's own gradient may be smaller than
  * that): pkm_vocab_loss_backward_with_loss takes the forward's loss beside lse, and has it as the training step
  * does.  A training step of more than some 76 * 2^16 logits saves a quarter of the products, in which a token's
- * factor is not 1 even where all dloss are the same; pkm_vocab_loss and pkm_vocab_loss_backward_with_loss, one
+ * factor is not 1 even where all dloss are the same (in dweight it takes back what the target's dz lost in rounding,
+ * and leaves as much in that row's others); pkm_vocab_loss and pkm_vocab_loss_backward_with_loss, one
  * after the other, are the same step with all products, and x as it is for a mean.
  *
  * workspace: device scratch of pkm_vocab_loss_workspace_bytes(B, dim, V) bytes, or of

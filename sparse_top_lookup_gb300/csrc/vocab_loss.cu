@@ -28,7 +28,7 @@
 // 8.3 so.
 //
 // Roundings besides the results': dz (E) and the scaled x, both bf16 operands of the tensor cores.  Off the
-// 64-bit results in the 2-norm: dx 2.4e-3, dW 2.9e-3 where powers are kept and 2.1e-3 in two passes of a
+// 64-bit results in the 2-norm: dx and dW 2.4e-3 where powers are kept and 2.1e-3 in two passes of a
 // mean's gradient (one rounding at the end 1.7e-3), the loss 9e-7.
 //
 // Bound by the tensor pipe in long products: a training step of 8192 x 2048 x 131072 runs at 1.7 PFLOP/s, what
@@ -162,6 +162,15 @@ __device__ __forceinline__ void scaled_row(const uint4* x, int vecs, float s, ui
 // what they are in two passes: bf16's range is 2^-126 to 2^127.
 constexpr float kLift = 0x1p20f;
 
+// Where powers are kept, x's copy is rounded with its row's factor anyway: the factor there also takes back what
+// rounding to bf16 changed of the target's power (exact / rounded), as a rule the row's largest element of dz by
+// far.  What is left of it is in the row's other elements (as much of each), and dW is 2.4e-3 off the 64-bit result
+// in the 2-norm instead of 2.9e-3 (4096 x 1024 x 32000).
+__device__ __forceinline__ float taken_back(float exact, __nv_bfloat16 rounded) {
+  const float q = __fdiv_rn(exact, __bfloat162float(rounded));
+  return q > 0.5f && q < 2.0f ? q : 1.0f;  // (0, infinities, NaN)
+}
+
 // What a piece's dloss are divided by in x's copy: that of its first token (of 32) that has one, if it is of a
 // size that leaves the others in range; else 1.  One warp; the same in every warp.
 __device__ __forceinline__ float common_factor(const int64_t* target, const float* dloss, int B, int V) {
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
     const float ref = kExps ? p.ref[mine] : reference(fmaxf(sum.top, zt));
     const float rest = kExps || sum.top == -INFINITY ? sum.sum : sum.sum * power(sum.top, ref);
     const float total = rest + power(zt, ref), lse = ref + logf(total);
-    float loss = 0.0f, scale = there && p.scaled ? p.dloss[mine] : 0.0f;
+    float loss = 0.0f, scale = there && p.scaled ? p.dloss[mine] : 0.0f, back = 1.0f;
     if (there) {
       // (of infinite logits: inf - inf is no number if the target's is one of them, a limit if it is not)
       if (total == INFINITY)
@@ -297,11 +306,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const JoinArgs p)
         *p.again = 1;
       }
       if (scale != 0.0f) {
-        p.exps[mine * p.pitch + t] = __float2bfloat16(expm1f(-loss) * total);
-        scale = scale / common / total;
+        const float own = expm1f(-loss) * total;
+        const __nv_bfloat16 rounded = __float2bfloat16(own);
+        p.exps[mine * p.pitch + t] = rounded;
+        scale = scale / common / total, back = taken_back(own, rounded);
       }
     }
-    if (p.scaled) p.row_scale[mine] = scale, scales[w] = scale;
+    if (p.scaled) p.row_scale[mine] = scale, scales[w] = scale * back;
     p.loss[mine] = loss;
     if (p.lse) p.lse[mine] = lse;
   }

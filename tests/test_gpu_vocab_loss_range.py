@@ -9,8 +9,8 @@ import pytest
 
 import sparse_top_lookup_gb300 as pk
 from more_operators64 import Guarded, vocab64
-from test_gpu_vocab_loss import (BF16, F64, HALF, check_gradient, check_loss, errors_of_logits,
-                                 forward, gradient, inputs, loss_bounds, near)
+from test_gpu_vocab_loss import (BF16, F64, HALF, check_loss, errors_of_logits, far, forward, gradient,
+                                 inputs, loss_bounds, near)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -116,6 +116,42 @@ def test_a_logit_of_minus_infinity(B, V, kind, move):
 # ------------------------------------------------------------------ weights
 
 
+def check_kept(x, w, target, dloss):
+    """The gradient's calls where a training step keeps powers.  dz is rounded once and the results are; x with
+    its factor once more, and in a training step that factor may take a rounding back: it is that of the
+    target's power, half a step of bf16 at most, and comes to the row's other elements instead.  Then an element
+    of dW is off by four half steps, each of what it sums, and one of dx by two."""
+    (B, dim), V = x.shape, w.shape[0]
+    assert -(-B // 256) * -(-V // 256) > 76
+    X, W = x.to(F64), w.to(F64)
+    loss, lse, e_loss, e_lse = loss_bounds(x, w, target)
+    _, _, dz = vocab64(X, W, target, dloss.to(F64))
+    Z = X @ W.T
+    ez = errors_of_logits(x, w) + 2.0 ** -23 * far(Z, target)
+    there = (target >= 0) & (target < V)
+    at = torch.where(there, target, torch.zeros_like(target))[:, None]
+    scale = torch.where(there, dloss.to(F64).abs(), torch.zeros_like(lse))[:, None]
+    p = torch.exp(Z - lse[:, None])
+    for train in (False, True):
+        el = (e_lse if train else torch.zeros_like(lse)) + 2.0 ** -24 * lse.abs()
+        eo = 1.05 * scale * p * (ez + el[:, None] + 2.0 ** -20)
+        if train:
+            eo = eo.scatter(1, at, 1.05 * scale * (e_loss + 2.0 ** -22 * -torch.expm1(-loss))[:, None])
+        edz = HALF * dz.abs() + eo
+        got = gradient(x, w, target, dloss, train, lse=lse.float())
+        if train:
+            check_loss(x, w, target, (got["loss"], got["lse"]))
+        sums = (V + 2) * 2.0 ** -24 * (dz.abs() @ W.abs())
+        want = dz @ W
+        near(got["dx"], want, 1.01 * (HALF * want.abs() + (1 + HALF) * (edz @ W.abs() + sums)) + 1e-38, 2,
+             "dx", eo @ W.abs() + sums)
+        sums = (B + 2) * 2.0 ** -24 * (dz.abs().T @ X.abs())
+        want = dz.T @ X
+        more = (2 if train else 1) * 1.01 * HALF * ((dz.abs() + edz).T @ X.abs())
+        each = HALF * want.abs() + (1 + HALF) * (edz.T @ X.abs() + sums + more)
+        near(got["dw"], want, 1.01 * each + 1e-38, 4 if train else 3, "dw", eo.T @ X.abs() + sums)
+
+
 def far_rows(B, dim, V, seed):
     """Tokens whose target lies 40 to 65 below their best logit."""
     x, w, target, _ = inputs(B, dim, V, seed=seed, absent=0.0, sd=7.0, lift=0.0)
@@ -136,7 +172,7 @@ def test_tokens_far_from_their_targets_with_small_weights(size, dim):
     B = 100
     x, w, target = far_rows(B, dim, 30000, seed=3)
     dloss = size * (0.5 + torch.rand(B, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)))
-    check_gradient(x, w, target, dloss)
+    check_kept(x, w, target, dloss)
 
 
 @pytest.mark.parametrize("first", [0.0, 1e-30, 1e30, math.nan])
@@ -144,12 +180,12 @@ def test_tokens_of_very_different_weight_in_a_step_that_keeps_powers(first):
     x, w, target, dloss = inputs(100, 64, 30000, seed=8, absent=0.0)
     target[:40] = -1
     dloss[:40] = first  # (padding: whatever it holds)
-    check_gradient(x, w, target, dloss)
+    check_kept(x, w, target, dloss)
     if first == 0.0:
         dloss[50], dloss[60:] = 1e-6, 1e-12
-        check_gradient(x, w, target, dloss)
+        check_kept(x, w, target, dloss)
         dloss[:] *= 1e-16
-        check_gradient(x, w, target, dloss)
+        check_kept(x, w, target, dloss)
 
 
 def test_one_light_token_far_from_its_target():
@@ -157,8 +193,29 @@ def test_one_light_token_far_from_its_target():
     x, w, target = far_rows(100, 64, 30000, seed=5)
     dloss = torch.full((100,), 1.0, device="cuda")
     dloss[1:] = 1e-10
-    check_gradient(x, w, target, dloss)
-    check_gradient(x, w, target, dloss.flip(0).contiguous())
+    check_kept(x, w, target, dloss)
+    check_kept(x, w, target, dloss.flip(0).contiguous())
+
+
+@pytest.mark.parametrize("B,dim,V", [(2000, 256, 10000), (500, 512, 30000)])
+def test_a_steps_dw_in_the_2_norm(B, dim, V):
+    # tokens learnt to some part: the target's element is most of dz, and its rounding is not in dW.  What is:
+    # x's with the factor and the result's, which are formed here, and both of the other elements' share
+    x, w, target, _ = inputs(B, dim, V, seed=1, absent=0.0, lift=math.log(V))
+    dloss = torch.full((B,), 1 / B, device="cuda")
+    X, W = x.to(F64), w.to(F64)
+    loss, lse, dz = vocab64(X, W, target, dloss.to(F64))
+    want = dz.T @ X
+    factor = (torch.exp((X * W[target]).sum(1) - lse) / B)[:, None]
+    xs = (X * factor).to(BF16).to(F64) / factor
+    fewest = (dz.T @ xs).to(BF16).to(F64) - want
+    size = X.square().sum(1)
+    own = dz.gather(1, target[:, None])[:, 0].square()
+    share = float(((dz.square().sum(1) - own) * size).sum() / (dz.square().sum(1) * size).sum())
+    dw = gradient(x, w, target, dloss, True)["dw"].to(F64)
+    off, norm = float((dw - want).norm() / want.norm()), float(fewest.norm() / want.norm())
+    assert off <= 1.03 * math.sqrt(norm ** 2 + 2 * share * HALF ** 2 / 3), (off, norm, share)
+
 
 
 # ------------------------------------------------------------------ learnt tokens
