@@ -667,7 +667,8 @@ int pkm_vocab_loss_train(const void *x, const void *weight, const int64_t *targe
  * pkm_usage_balance: counts [H][2][n_keys] int32, mass [H][2][n_keys] fp32, loss [H] fp32, each
  * overwritten, each NULL where it is not wanted.  Weights lie in [0, 1], as a softmax's do; one that
  * does not (beyond 1 + 2^-10, NaN) makes its head's mass and loss NaN.  Masses are summed as
- * whole numbers of 2^-31: the same bits every time.  workspace: device
+ * whole numbers of 2^-31, to which each weight is rounded (one below 2^-32 adds nothing to its subkeys'): the
+ * same bits every time.  workspace: device
  * scratch of pkm_usage_balance_workspace_bytes(H, n_keys) bytes, caller-owned, 16-byte aligned; it
  * holds nothing between calls.  A head without entries has loss 0.
  *

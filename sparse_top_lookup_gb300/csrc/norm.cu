@@ -7,10 +7,12 @@
 // d is the gradient of s, so of x and of r alike.  Everything between the loads and the stores is
 // fp32; y comes from the unrounded s.
 //
-// Bound by HBM in large batches: 16384 x 2048, bf16 all through, 40.5 us (98 % of the copy), fp32 stream
+// Bound by HBM in large batches: 16384 x 2048, bf16 all through, 40.6 us (97 % of the copy), fp32 stream
 // with an fp8 result 68 (94 %); the backward pass 50 (80 %): its 16 warps an SM, of 120 registers, leave
 // issue slots empty (58 % used) while loads are on their way.  Rows ahead in shared memory (61 to 69), more
-// warps of fewer registers (61) and packed arithmetic (52) were slower.  Small ones by the launch (4 us).
+// warps of fewer registers (61) and packed arithmetic (52) were slower.  Small ones by the launch (4 us).  The
+// backward pass of rows above 8192 columns by its registers: the next row beside this one, four vectors of each a
+// thread, spills (4096 x 16384 bf16 173 us, 46 % of the copy, an fp32 stream 425 and 33 %, fp32 all through 1148 and 14 %).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <float.h>
@@ -402,7 +404,8 @@ norm_join_kernel(const float* __restrict__ parts, int count, int dim, float* out
 
 // A row's warps (a power of two) and vectors a thread: two, or four where a row is longer than 512 threads
 // take so.  One vector (256 threads, 2048 columns) left too little on its way: 16384 x 2048 with an fp8
-// result 88 us (two 69), bf16 59 (44); four 79 and 41, and too many registers in the backward pass.
+// result 88 us (two 69), bf16 59 (44); four 79 and 41, and too many registers in the backward pass, which rows
+// above 8192 columns pay for.
 // Blocks of 512 threads suit rows of 16 bits (bf16 44 -> 41 us, 97 % of the copy; fp32 69 -> 73), as
 // the GPU starts only so many blocks a microsecond (of 128 threads: 62 and 95).
 struct Shape {

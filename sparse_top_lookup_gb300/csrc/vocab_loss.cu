@@ -22,18 +22,18 @@
 // target's logit, which is known before, and the sums are known after it: dz = dloss exp(r - lse) E beside
 // the target, whose element the join writes.  That factor takes dloss's place, so nothing passes over E
 // again; it may be 2^-100 of dloss, so the common factor stays out of it here too, and dx's rows are multiplied
-// by the one and the other.  E holds for a row whose sum stays below 2^100; when one of a piece does not (its best logit is 69
-// above the target's), the join takes that row's maximum for its reference and raises a mark, and two
+// by the one and the other.  E holds for a row whose sum stays below 2^100; when one of a piece does not (its best
+// logit is 69 above the target's), the join takes that row's maximum for its reference and raises a mark, and two
 // launches that do nothing otherwise (7 us) do the piece again.  8192 x 2048 x 131072: 10.7 ms in two passes,
-// 8.3 so.
+// 7.7 to 8.3 so (one GPU and another).
 //
 // Roundings besides the results': dz (E) and the scaled x, both bf16 operands of the tensor cores.  Off the
 // 64-bit results in the 2-norm: dx and dW 2.4e-3 where powers are kept and 2.1e-3 in two passes of a
 // mean's gradient (one rounding at the end 1.7e-3), the loss 9e-7.
 //
-// Bound by the tensor pipe in long products: a training step of 8192 x 2048 x 131072 runs at 1.7 PFLOP/s, what
-// cuBLAS sustains under the power limit; 83 % of the pipe's cycles in dx and dW at 4096 x 1024 x 32000,
-// 74 % in the logits (27 rounds of tiles where 26.3 would do, and an epilogue of 2.9 us a tile beside 5.2 of
+// Bound by the tensor pipe in long products: a training step of 8192 x 2048 x 131072 runs at 1.6 to 1.7 PFLOP/s, 93
+// to 99 % of what cuBLAS sustains under the power limit; 84 % of the pipe's cycles in dx and dW at 4096 x 1024 x
+// 32000, 76 % in the logits (27 rounds of tiles where 26.3 would do, and an epilogue of 2.9 us a tile beside 5.2 of
 // products).  Short products (dim below 512) by that epilogue; few tokens by W's reading and dW's writing.
 #include <math.h>
 #include <stdint.h>
@@ -472,8 +472,8 @@ Pieces pieces_of(int B, int dim, int V, int grad_dtype) {
 bool small_step(int B, int V) { return ((int64_t)B + 255) / 256 * (((int64_t)V + 255) / 256) <= kPairs; }
 
 // A training step's pieces: all of a piece's E at once.  Several pieces need dW's sums in fp32 (unless dW
-// is): where those would take as much as the rest of E, it is one piece (8192 x 2048 x 131072, two of 1 GiB
-// and 1 GiB of sums 8.35 ms, one of 2 GiB 8.05).
+// is): where those would take as much as the rest of E, it is one piece (8192 x 2048 x 131072 on one GPU: two of
+// 1 GiB and 1 GiB of sums 8.35 ms, one of 2 GiB 8.05).
 int train_tokens(int B, int dim, int V, int grad_dtype) {
   const int64_t row = 2 * (int64_t)pitch16(V), sums = grad_dtype == PKM_BF16 ? 4 * (int64_t)V * dim : 0;
   if (row * B <= kPieceBytes + sums) return B;
