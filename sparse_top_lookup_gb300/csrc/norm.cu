@@ -12,7 +12,8 @@
 // issue slots empty (58 % used) while loads are on their way.  Rows ahead in shared memory (61 to 69), more
 // warps of fewer registers (61) and packed arithmetic (52) were slower.  Small ones by the launch (4 us).  The
 // backward pass of rows above 8192 columns by its registers: the next row beside this one, four vectors of each a
-// thread, spills (4096 x 16384 bf16 173 us, 46 % of the copy, an fp32 stream 425 and 33 %, fp32 all through 1148 and 14 %).
+// thread, spills (4096 x 16384 bf16 173 us, 46 % of the copy, an fp32 stream 428 and 32 %, fp32 all through
+// 1165 and 14 %).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <float.h>

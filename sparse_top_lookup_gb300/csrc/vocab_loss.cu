@@ -12,10 +12,10 @@
 //
 // Backward: z is computed again, and its epilogue writes dz / dloss = exp(z - lse) - [target] in bf16,
 // piece by piece (of the tokens, and of the vocabulary within), then dx and dW of the piece in one
-// launch; the target's own, exp(-loss) - 1, comes from the forward's loss, or from lse and once more an fp32 sum for
-// its logit, which leaves in it what lse is off by (2^-24 of it from its rounding alone); dloss multiplies dx's rows in fp32, and x in dW's operand, over what most tokens' dloss is in a
-// mean (common_factor, which multiplies dW in fp32): x is rounded once more only where tokens weigh
-// differently.
+// launch.  The target's own, exp(-loss) - 1, comes from the forward's loss, or from lse and once more an
+// fp32 sum for its logit, which leaves in it what lse is off by (2^-24 of it from its rounding alone).  dloss
+// multiplies dx's rows in fp32, and x in dW's operand, over what most tokens' dloss is in a mean
+// (common_factor, which multiplies dW in fp32): x is rounded once more only where tokens weigh differently.
 //
 // Training, where the logits are more than one round of tiles: a quarter of the products can be saved.  The
 // loss's epilogue writes E = exp(z - r) in bf16 against a reference r of its own for each token, the
