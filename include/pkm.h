@@ -610,7 +610,9 @@ int pkm_add_rms_norm_backward(const void *sum, int sum_dtype, const float *weigh
  * (either may be NULL: not computed; grad_dtype PKM_BF16: dweight overwritten; PKM_F32: fp32, added to)
  * from the forward's lse and the loss's gradient dloss; z is computed again.  pkm_vocab_loss_train: all of it
  * in one call, for a training step that knows dloss beforehand (1 / B for a mean).  dz is rounded to bf16
- * once, as an operand of the tensor cores, and so is x times its token's factor, where it is not 1.
+ * once, as an operand of the tensor cores, and so is x times its token's factor, where it is not 1.  The logits
+ * beside the target's are the tensor cores' sums, which cut low bits off: lse is below what fp32 sums give by some
+ * 5e-7 of the largest logits (1e-6 of the loss, as a rule).
  *
  * A target's own exp(z - lse) - 1 is good relative to itself in the training step.  From lse alone it is off by
  * what lse is (by its rounding, 2^-24 of it, at the least: a learnt token's own gradient may be smaller than
